@@ -1,0 +1,156 @@
+"""include/sage_sparse.h: symbols, binding signatures and refusals, all on the host (no GPU needed)."""
+import ctypes
+import re
+
+import pytest
+import torch
+
+from video_dit_quantized_b200 import sage, sparse
+
+EXPECTED = {"sage_qk_norm_rope", "sage_select_scratch_bytes", "sage_select_blocks", "sage_attn_fwd_sparse",
+            "sage_dbg_sparse_forced_timeout"}
+VP = ctypes.c_void_p
+
+
+def test_header_and_libraries_agree():
+    assert set(sparse.header_functions()) == EXPECTED
+    for lib in (sage.LIB, sage.debug_library()):
+        for name in EXPECTED:
+            assert hasattr(lib, name), name
+
+
+def test_binding_signatures_match_the_header():
+    txt = re.sub(r"/\*.*?\*/", "", open(sparse.HEADER).read(), flags=re.S)
+    kinds = {"int": ctypes.c_int, "size_t": ctypes.c_size_t, "long long": ctypes.c_longlong, "double": ctypes.c_double}
+    seen = set()
+    for m in re.finditer(r"^(int|size_t)\s+(sage_\w+)\(([^)]*)\);", txt, flags=re.M):
+        ret, name, params = m.groups()
+        want = [VP if "*" in p else kinds[" ".join(p.split()[:-1])] for p in params.split(",")]
+        f = getattr(sage.LIB, name)
+        assert list(f.argtypes) == want and f.restype == kinds[ret], name
+        seen.add(name)
+    assert seen == EXPECTED
+
+
+def test_header_constants_match_the_binding():
+    txt = open(sparse.HEADER).read()
+    value = lambda n: int(re.search(rf"#define SAGE_{n} (\d+)", txt).group(1))
+    for name in ("NORM_NONE", "NORM_RMS", "NORM_LAYER", "NORM_SCOPE_HEAD", "NORM_SCOPE_ALL", "ROPE_NONE",
+                 "ROPE_INTERLEAVED", "ROPE_HALF", "NORM_MAX_WIDTH", "SELECT_MAX_BLOCKS"):
+        assert value(name) == getattr(sparse, name), name
+
+
+def _norm_args(**kw):
+    a = dict(q=1 << 30, k=2 << 30, qs=512, ks=512, wq=3 << 30, bq=None, wk=3 << 30, bk=None, wd=0, cos=4 << 30,
+             sin=5 << 30, B=2, N=100, H=4, d=128, norm=sparse.NORM_RMS, scope=0, eps=1e-6, rope=1, begin=0, len=100,
+             qo=6 << 30, ko=7 << 30, ranks=0)
+    a.update(kw)
+    return list(a.values()) + [None]
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(B=0), sage.EINVAL), (dict(N=0), sage.EINVAL), (dict(H=0), sage.EINVAL), (dict(d=96), sage.EUNSUPPORTED),
+    (dict(H=129, qs=129 * 128, ks=129 * 128), sage.EUNSUPPORTED), (dict(B=1 << 20, N=1 << 12), sage.EINVAL),
+    (dict(norm=3), sage.EINVAL), (dict(norm=-1), sage.EINVAL), (dict(scope=2), sage.EINVAL), (dict(rope=3), sage.EINVAL),
+    (dict(wd=2), sage.EINVAL), (dict(eps=-1.0), sage.EINVAL), (dict(eps=float("nan")), sage.EINVAL),
+    (dict(eps=1e300), sage.EINVAL), (dict(begin=-1), sage.EINVAL), (dict(begin=1), sage.EINVAL),
+    (dict(begin=2 ** 31 - 1, len=2 ** 31 - 1), sage.EINVAL), (dict(len=-1), sage.EINVAL), (dict(cos=None), sage.EINVAL),
+    (dict(sin=(5 << 30) + 8), sage.EINVAL), (dict(ranks=3), sage.EINVAL), (dict(ranks=-1), sage.EINVAL),
+    (dict(q=None), sage.EINVAL),                                     # its output and weight remain
+    (dict(q=None, qo=None, wq=None, k=None, ko=None, wk=None), sage.EINVAL),
+    (dict(qs=504), sage.EINVAL), (dict(qs=516), sage.EINVAL), (dict(qs=1 << 60), sage.EINVAL),
+    (dict(q=(1 << 30) + 8), sage.EINVAL), (dict(qo=(6 << 30) + 8), sage.EINVAL), (dict(wq=(3 << 30) + 8), sage.EINVAL),
+    (dict(bq=3 << 30), sage.EINVAL),                                 # RMS has no bias
+    (dict(norm=0), sage.EINVAL),                                     # no norm has no weight
+    (dict(qo=1 << 30), sage.EINVAL),                                 # onto the input, another layout
+    (dict(qo=1 << 30, ranks=1, qs=1024), sage.EINVAL),               # onto a strided input
+    (dict(qo=(1 << 30) + 1024, ranks=1), sage.EINVAL),               # shifted onto the input
+    (dict(qo=2 << 30, ranks=1), sage.EINVAL),                        # onto the other input
+    (dict(ko=6 << 30), sage.EINVAL), (dict(ko=4 << 30), sage.EINVAL), (dict(ko=3 << 30), sage.EINVAL),
+])
+def test_norm_rope_refusals(kw, code):
+    assert sage.LIB.sage_qk_norm_rope(*_norm_args(**kw)) == code
+
+
+def test_norm_rope_in_place_and_well_formed_calls_reach_the_device_check():
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up")
+    for kw in (dict(), dict(qo=1 << 30, ko=2 << 30, ranks=1), dict(q=None, qo=None, wq=None), dict(len=0, cos=None, sin=None),
+               dict(rope=0, cos=None, sin=None), dict(ranks=4), dict(norm=2, bq=8 << 30)):
+        assert sage.LIB.sage_qk_norm_rope(*_norm_args(**kw)) in (sage.ELAUNCH, sage.EUNSUPPORTED), kw
+
+
+def test_select_refusals():
+    f = sage.LIB.sage_select_blocks
+    a, odd = VP(1 << 30), VP((1 << 30) + 8)
+    n = sparse.select_scratch_bytes(1, 2, 1000, 128)
+    assert n == 2 * 2 * 8 * 128 * 4
+    ok = lambda q=a, k=a, B=1, H=2, N=1000, d=128, keep=3, first=0, window=0, li=a, co=a, sc=a, nb=n: f(
+        q, k, B, H, N, d, keep, first, window, li, co, sc, nb, None)
+    for kw in (dict(q=None), dict(k=odd), dict(B=0), dict(N=0), dict(keep=0), dict(first=-1), dict(window=-2),
+               dict(window=2), dict(first=3), dict(first=2 ** 31 - 1, window=2 ** 31 - 1), dict(li=None), dict(co=VP(6)),
+               dict(sc=odd), dict(H=70000)):
+        assert ok(**kw) == sage.EINVAL, kw
+    assert ok(d=96) == sage.EUNSUPPORTED
+    assert ok(nb=n - 1) == sage.EWORKSPACE
+    most = sparse.SELECT_MAX_BLOCKS * 128
+    assert ok(N=most + 1) == sage.EUNSUPPORTED
+    assert sparse.select_scratch_bytes(1, 1, most, 64) > 0 and sparse.select_scratch_bytes(1, 1, most + 1, 64) == 0
+    with pytest.raises(sage.SageError):
+        sparse.alloc_select_scratch(1, 1, most + 1, 64)
+    if not torch.cuda.is_available():
+        assert ok() in (sage.ELAUNCH, sage.EUNSUPPORTED)
+        assert ok(keep=8, first=9, window=9) in (sage.ELAUNCH, sage.EUNSUPPORTED)     # every block is kept
+
+
+def test_sparse_refusals():
+    n = sage.workspace_bytes(1, 2, 1000, 128, sage.MODE_INT8_FP8)
+    base = dict(q=1 << 30, k=2 << 30, v=3 << 30, o=4 << 30, B=1, H=2, N=1000, d=128, mode=1, li=5 << 30, co=6 << 30,
+                width=3, ws=7 << 30, nb=n)
+    call = lambda **kw: sage.LIB.sage_attn_fwd_sparse(*{**base, **kw}.values(), None)
+    for kw in (dict(q=None), dict(v=(3 << 30) + 8), dict(N=0), dict(mode=3), dict(mode=-1), dict(width=0), dict(li=None),
+               dict(co=(6 << 30) + 2), dict(ws=(7 << 30) + 16), dict(o=1 << 30), dict(o=(2 << 30) + 1024),
+               dict(o=5 << 30), dict(o=6 << 30), dict(o=7 << 30), dict(H=70000)):
+        assert call(**kw) == sage.EINVAL, kw
+    assert call(d=32) == sage.EUNSUPPORTED
+    assert call(nb=n - 1) == sage.EWORKSPACE
+    dbg = lambda cycles: sage.LIB.sage_dbg_sparse_forced_timeout(*base.values(), cycles, None)
+    assert dbg(10) == sage.EINVAL and dbg(1 << 60) == sage.EINVAL
+    if not torch.cuda.is_available():
+        assert call() in (sage.ELAUNCH, sage.EUNSUPPORTED)
+
+
+def test_binding_refuses_what_the_c_abi_cannot_see():
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    q = bf(1, 200, 2, 64)
+    t = torch.zeros(200, 32)
+    for match, args, kw in (
+            ("required", (None,), {}), (r"\[B, N, H, d\]", (q[0],), {}), ("bfloat16", (q.float(),), {}),
+            ("must not be empty", (q[:, :0],), {}),
+            ("shape", (q, bf(1, 100, 2, 64)), {}), ("contiguous", (q.transpose(1, 2),), {}),
+            ("contiguous", (q[:, :, :, :32],), {}), ("evenly", (bf(2, 300, 2, 64)[:, :200],), {}),
+            ("float32", (q,), dict(cos=t.double(), sin=t.double())), ("shape", (q,), dict(cos=t, sin=t[:, :16].contiguous())),
+            ("required", (q,), dict(cos=t)), ("shape", (q,), dict(wq=bf(128))), ("all", (q, q), dict(wq=bf(64), wk=torch.zeros(64))),
+            ("all", (q,), dict(wq=torch.zeros(64, dtype=torch.float16))), ("no input", (q,), dict(k_out=bf(1, 2, 200, 64))),
+            ("shape", (q,), dict(q_out=bf(1, 200, 2, 64))), ("multiple", (q,), dict(ranks=3)),
+            ("not a CUDA tensor", (q, q), dict(wq=bf(64), wk=bf(64), cos=t, sin=t))):
+        with pytest.raises(ValueError, match=match):
+            sparse.qk_norm_rope(*args, **kw)
+    q = bf(1, 2, 200, 64)
+    li, co = torch.zeros(1, 2, 2, 1, dtype=torch.int32), torch.zeros(1, 2, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="keep"):
+        sparse.select_blocks(q, q, 0)
+    with pytest.raises(ValueError, match="shape"):
+        sparse.select_blocks(q, q, 2, lists=li)
+    with pytest.raises(ValueError, match="bfloat16"):
+        sparse.select_blocks(q, q.float(), 1)
+    with pytest.raises(ValueError, match="not a CUDA tensor"):
+        sparse.select_blocks(q, q, 1)
+    with pytest.raises(ValueError, match="shape"):
+        sparse.attn_fwd_sparse(q, q, q, 0, li[:, :1].contiguous(), co)
+    with pytest.raises(ValueError, match="int32"):
+        sparse.attn_fwd_sparse(q, q, q, 0, li.long(), co)
+    with pytest.raises(ValueError, match="shape"):
+        sparse.attn_fwd_sparse(q, q, q, 0, li, co[:, :1].contiguous())
+    with pytest.raises(ValueError, match="not a CUDA tensor"):
+        sparse.attn_fwd_sparse(q, q, q, 0, li, co)

@@ -8,8 +8,10 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
-SOURCES = ["api.cu", "prepass.cu", "attention.cu", "noalloc.cu", "calib.cu", "linear.cu", "ulysses.cu", "diag.cu"]
-HEADERS = ["internal.h", "sm100.cuh"]
+SOURCES = ["api.cu", "prepass.cu", "attention.cu", "noalloc.cu", "calib.cu", "linear.cu", "ulysses.cu", "diag.cu",
+           "norm_rope.cu", "select.cu", "sparse.cu"]
+HEADERS = ["internal.h", "sm100.cuh", "attn_tiles.cuh"]
+PUBLIC_HEADERS = ["sage.h", "sage_sparse.h"]
 LIB_PATH = os.path.join(HERE, "libsage.so")
 # the same sources with device-side bounds checks (SAGE_DEBUG, see include/sage.h)
 DEBUG_LIB_PATH = os.path.join(HERE, "libsage_debug.so")
@@ -26,8 +28,8 @@ def _stale(path: str) -> bool:
     if not os.path.exists(path):
         return True
     t = os.path.getmtime(path)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", "sage.h"),
-                                                                  os.path.abspath(__file__)]
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", f) for f in PUBLIC_HEADERS]
+    deps.append(os.path.abspath(__file__))
     return any(os.path.getmtime(p) > t for p in deps)
 
 

@@ -1,4 +1,5 @@
-// api.cu -- the extern "C" entry points declared in include/sage.h: argument
+// api.cu -- the extern "C" entry points declared in include/sage.h and
+// include/sage_sparse.h: argument
 // validation, workspace layout, TMA tensor-map encoding and kernel launches.
 // Marshalling only; every step of the computation runs in the kernels of
 // prepass.cu and attention.cu.
@@ -8,10 +9,12 @@
 
 #include <cstdint>
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
 #include "../../include/sage.h"
+#include "../../include/sage_sparse.h"
 #include "internal.h"
 
 namespace sage {
@@ -54,6 +57,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Side streams and events of sage_attn_fwd_host, made on first use per device
 // (and again in a new CUDA context) and kept for the life of the process.  A
@@ -124,6 +128,25 @@ Layout layout(int B, int H, int N, int d, bool q_per_token = false) {
   return L;
 }
 
+// The prepass outputs inside a workspace laid out by layout().
+struct Operands {
+  int8_t *q_i8, *k_i8;
+  uint8_t* v_f8t;
+  float *q_scale, *k_scale, *k_mean, *v_scale;
+  PrepassScratch scratch;
+  Operands(char* ws, int B, int H, int N, int d, bool q_per_token) {
+    const Layout L = layout(B, H, N, d, q_per_token);
+    q_i8 = reinterpret_cast<int8_t*>(ws + L.q_i8);
+    k_i8 = reinterpret_cast<int8_t*>(ws + L.k_i8);
+    v_f8t = reinterpret_cast<uint8_t*>(ws + L.v_f8t);
+    q_scale = reinterpret_cast<float*>(ws + L.q_scale);
+    k_scale = reinterpret_cast<float*>(ws + L.k_scale);
+    k_mean = reinterpret_cast<float*>(ws + L.k_mean);
+    v_scale = reinterpret_cast<float*>(ws + L.v_scale);
+    scratch = prepass_scratch_carve(ws + L.scratch, B * H, N, d);
+  }
+};
+
 int check_shape(int B, int H, int N, int d) {
   if (B < 1 || H < 1 || N < 1) return SAGE_EINVAL;
   if (d != 64 && d != 128) return SAGE_EUNSUPPORTED;
@@ -165,7 +188,8 @@ int debug_collect(cudaStream_t st, int rc) {
   if (cudaStreamSynchronize(st) != cudaSuccess) return SAGE_ELAUNCH;
   std::lock_guard<std::mutex> lock(g_debug_mu);
   unsigned long long first = 0;
-  const unsigned w = debug_take_prepass(&first) | debug_take_attention(&first) | debug_take_ulysses(&first);
+  const unsigned w = debug_take_prepass(&first) | debug_take_attention(&first) | debug_take_ulysses(&first) |
+                     debug_take_norm_rope(&first) | debug_take_select(&first) | debug_take_sparse(&first);
   if (w) {
     g_debug_first = first;
     return SAGE_EBOUNDS;
@@ -276,20 +300,13 @@ namespace {
 int run_quantized(const void* q, const void* k, const void* v, void* o, int B, int H, int N, int d, bool qtok,
                   char* ws, cudaStream_t st, RowMap in_map, RowMap o_map) {
   uint32_t* status = reinterpret_cast<uint32_t*>(ws);
-  const Layout L = layout(B, H, N, d, qtok);
-  auto q_i8 = reinterpret_cast<int8_t*>(ws + L.q_i8);
-  auto k_i8 = reinterpret_cast<int8_t*>(ws + L.k_i8);
-  auto v_f8t = reinterpret_cast<uint8_t*>(ws + L.v_f8t);
-  auto q_scale = reinterpret_cast<float*>(ws + L.q_scale);
-  auto k_scale = reinterpret_cast<float*>(ws + L.k_scale);
-  auto k_mean = reinterpret_cast<float*>(ws + L.k_mean);
-  auto v_scale = reinterpret_cast<float*>(ws + L.v_scale);
-  const PrepassScratch s = prepass_scratch_carve(ws + L.scratch, B * H, N, d);
-  cudaError_t e =
-      launch_prepass(q, k, v, B * H, N, d, q_i8, q_scale, k_i8, k_scale, k_mean, v_f8t, v_scale, s, st, qtok, in_map);
+  const Operands op(ws, B, H, N, d, qtok);
+  const cudaError_t e = launch_prepass(q, k, v, B * H, N, d, op.q_i8, op.q_scale, op.k_i8, op.k_scale, op.k_mean,
+                                       op.v_f8t, op.v_scale, op.scratch, st, qtok, in_map);
   if (e != cudaSuccess) return launch_status(e);
-  return debug_collect(st, launch_status(launch_attn_i8f8(q_i8, q_scale, k_i8, k_scale, v_f8t, v_scale, o, B * H, N,
-                                                          d, status, kDefaultTimeoutCycles, 0, st, qtok, o_map)));
+  return debug_collect(st, launch_status(launch_attn_i8f8(op.q_i8, op.q_scale, op.k_i8, op.k_scale, op.v_f8t,
+                                                          op.v_scale, o, B * H, N, d, status, kDefaultTimeoutCycles, 0,
+                                                          st, qtok, o_map)));
 }
 }  // namespace
 }  // namespace sage
@@ -313,6 +330,157 @@ int sage_attn_fwd(const void* q, const void* k, const void* v, void* o, int B, i
                                                             st)));
   const RowMap plain{0, 0, 0, 0};
   return run_quantized(q, k, v, o, B, H, N, d, mode == SAGE_MODE_INT8_FP8_QTOKEN, ws, st, plain, plain);
+}
+
+namespace {
+
+// Whether two buffers share a byte.
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
+// One of the two tensors of sage_qk_norm_rope.
+int check_norm_tensor(const void* x, long long stride, const void* w, const void* b, const void* y, long long tokens,
+                      int width, int norm) {
+  if (!x || !y || !aligned16(x) || !aligned16(y) || stride < width || stride % 8 != 0) return SAGE_EINVAL;
+  if (stride > (1LL << 40) / tokens) return SAGE_EINVAL;        // 2^41 bytes: no buffer is that long
+  if ((w && !aligned16(w)) || (b && !aligned16(b))) return SAGE_EINVAL;
+  if (norm == SAGE_NORM_NONE ? (w || b) : (norm == SAGE_NORM_RMS && b)) return SAGE_EINVAL;
+  return SAGE_OK;
+}
+
+int check_sparse(const void* q, const void* k, const void* v, void* o, int B, int H, int N, int d, int mode,
+                 const int32_t* lists, const int32_t* counts, int width, void* workspace, size_t workspace_bytes) {
+  const int rc = check_shape(B, H, N, d);
+  if (rc != SAGE_OK) return rc;
+  if (mode != SAGE_MODE_BF16 && mode != SAGE_MODE_INT8_FP8 && mode != SAGE_MODE_INT8_FP8_QTOKEN) return SAGE_EINVAL;
+  if (width < 1) return SAGE_EINVAL;
+  const void* ptrs[] = {q, k, v, o, workspace};
+  for (const void* p : ptrs)
+    if (!p || !aligned16(p)) return SAGE_EINVAL;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SAGE_EINVAL;
+  if (!lists || !counts || !aligned4(lists) || !aligned4(counts)) return SAGE_EINVAL;
+  if (workspace_bytes < sage_workspace_bytes(B, H, N, d, mode)) return SAGE_EWORKSPACE;
+  const size_t tensor = (size_t)B * H * N * d * 2, rows = (size_t)B * H * num_tiles(N);
+  if (overlap(o, tensor, q, tensor) || overlap(o, tensor, k, tensor) || overlap(o, tensor, v, tensor) ||
+      overlap(o, tensor, lists, rows * width * 4) || overlap(o, tensor, counts, rows * 4) ||
+      overlap(o, tensor, workspace, sage_workspace_bytes(B, H, N, d, mode)))
+    return SAGE_EINVAL;
+  return check_device();
+}
+
+int run_sparse(const void* q, const void* k, const void* v, void* o, int B, int H, int N, int d, int mode,
+               const int32_t* lists, const int32_t* counts, int width, char* ws, long long timeout_cycles,
+               int dbg_flags, cudaStream_t st) {
+  uint32_t* status = reinterpret_cast<uint32_t*>(ws);
+  if (mode == SAGE_MODE_BF16)
+    return debug_collect(st, launch_status(launch_sparse_bf16(q, k, v, o, B * H, N, d, lists, counts, width, status,
+                                                              timeout_cycles, dbg_flags, st)));
+  const bool qtok = mode == SAGE_MODE_INT8_FP8_QTOKEN;
+  const Operands op(ws, B, H, N, d, qtok);
+  const RowMap plain{0, 0, 0, 0};
+  const cudaError_t e = launch_prepass(q, k, v, B * H, N, d, op.q_i8, op.q_scale, op.k_i8, op.k_scale, op.k_mean,
+                                       op.v_f8t, op.v_scale, op.scratch, st, qtok, plain);
+  if (e != cudaSuccess) return launch_status(e);
+  return debug_collect(st, launch_status(launch_sparse_i8f8(op.q_i8, op.q_scale, op.k_i8, op.k_scale, op.v_f8t,
+                                                            op.v_scale, o, B * H, N, d, lists, counts, width, status,
+                                                            timeout_cycles, dbg_flags, st, qtok)));
+}
+
+}  // namespace
+
+int sage_qk_norm_rope(const void* q, const void* k, long long q_stride, long long k_stride, const void* wq,
+                      const void* bq, const void* wk, const void* bk, int w_dtype, const float* cos, const float* sin,
+                      int B, int N, int H, int d, int norm, int scope, double eps, int rope, int rope_begin,
+                      int rope_len, void* q_out, void* k_out, int out_ranks, void* stream) {
+  if (B < 1 || H < 1 || N < 1 || (long long)B * N >= (1LL << 31)) return SAGE_EINVAL;
+  if (d != 64 && d != 128) return SAGE_EUNSUPPORTED;
+  if (H > SAGE_NORM_MAX_WIDTH / d) return SAGE_EUNSUPPORTED;
+  if (norm < SAGE_NORM_NONE || norm > SAGE_NORM_LAYER || scope < SAGE_NORM_SCOPE_HEAD || scope > SAGE_NORM_SCOPE_ALL ||
+      rope < SAGE_ROPE_NONE || rope > SAGE_ROPE_HALF)
+    return SAGE_EINVAL;
+  if (w_dtype != SAGE_DTYPE_BF16 && w_dtype != SAGE_DTYPE_F32) return SAGE_EINVAL;
+  if (!std::isfinite((float)eps) || eps < 0.0) return SAGE_EINVAL;
+  if (rope_begin < 0 || rope_len < 0 || (long long)rope_begin + rope_len > N) return SAGE_EINVAL;
+  if (rope != SAGE_ROPE_NONE && rope_len > 0 && (!cos || !sin || !aligned16(cos) || !aligned16(sin))) return SAGE_EINVAL;
+  if (out_ranks < 0 || (out_ranks > 0 && H % out_ranks != 0)) return SAGE_EINVAL;
+  if ((!q && !k) || (!q && (q_out || wq || bq)) || (!k && (k_out || wk || bk))) return SAGE_EINVAL;
+  const int width = H * d;
+  const long long tokens = (long long)B * N;
+  int rc = SAGE_OK;
+  if (q && (rc = check_norm_tensor(q, q_stride, wq, bq, q_out, tokens, width, norm)) != SAGE_OK) return rc;
+  if (k && (rc = check_norm_tensor(k, k_stride, wk, bk, k_out, tokens, width, norm)) != SAGE_OK) return rc;
+  const size_t out_bytes = (size_t)tokens * width * 2, table = (size_t)rope_len * d * 2;
+  const size_t w_bytes = (size_t)(scope == SAGE_NORM_SCOPE_ALL ? width : d) * (w_dtype == SAGE_DTYPE_F32 ? 4 : 2);
+  const void* outs[2] = {q_out, k_out};
+  const void* ins[2] = {q, k};
+  const long long strides[2] = {q_stride, k_stride};
+  const void* vecs[4] = {wq, bq, wk, bk};
+  for (int a = 0; a < 2; ++a) {
+    if (!outs[a]) continue;
+    for (int b = 0; b < 2; ++b) {
+      if (!ins[b]) continue;
+      const bool in_place = a == b && outs[a] == ins[b] && out_ranks == 1 && strides[b] == width;
+      const size_t in_bytes = ((size_t)(tokens - 1) * strides[b] + width) * 2;
+      if (!in_place && overlap(outs[a], out_bytes, ins[b], in_bytes)) return SAGE_EINVAL;
+    }
+    if (rope != SAGE_ROPE_NONE && rope_len > 0 &&
+        (overlap(outs[a], out_bytes, cos, table) || overlap(outs[a], out_bytes, sin, table)))
+      return SAGE_EINVAL;
+    for (const void* w : vecs)
+      if (w && overlap(outs[a], out_bytes, w, w_bytes)) return SAGE_EINVAL;
+  }
+  if (q_out && k_out && overlap(q_out, out_bytes, k_out, out_bytes)) return SAGE_EINVAL;
+  if ((rc = check_device()) != SAGE_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return debug_collect(st, launch_status(launch_qk_norm_rope(
+                               q, k, q_stride, k_stride, wq, bq, wk, bk, w_dtype == SAGE_DTYPE_F32, cos, sin, B, N, H,
+                               d, norm, scope == SAGE_NORM_SCOPE_ALL, (float)eps, rope, rope_begin, rope_len, q_out,
+                               k_out, out_ranks, st)));
+}
+
+size_t sage_select_scratch_bytes(int B, int H, int N, int d) {
+  if (check_shape(B, H, N, d) != SAGE_OK || num_tiles(N) > SAGE_SELECT_MAX_BLOCKS) return 0;
+  return select_scratch_bytes(B * H, N, d);
+}
+
+int sage_select_blocks(const void* q, const void* k, int B, int H, int N, int d, int keep, int first, int window,
+                       int32_t* lists, int32_t* counts, void* scratch, size_t scratch_bytes, void* stream) {
+  int rc = check_shape(B, H, N, d);
+  if (rc != SAGE_OK) return rc;
+  const int nT = num_tiles(N);
+  if (nT > SAGE_SELECT_MAX_BLOCKS) return SAGE_EUNSUPPORTED;
+  if (keep < 1 || first < 0 || window < -1) return SAGE_EINVAL;
+  if (keep < nT && (long long)first + (window < 0 ? 0 : 2LL * window + 1) > keep) return SAGE_EINVAL;
+  const void* ptrs[] = {q, k, scratch};
+  for (const void* p : ptrs)
+    if (!p || !aligned16(p)) return SAGE_EINVAL;
+  if (!lists || !counts || !aligned4(lists) || !aligned4(counts)) return SAGE_EINVAL;
+  if (scratch_bytes < select_scratch_bytes(B * H, N, d)) return SAGE_EWORKSPACE;
+  if ((rc = check_device()) != SAGE_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return debug_collect(st, launch_status(launch_select_blocks(q, k, B * H, N, d, keep, first, window, lists, counts,
+                                                              scratch, st)));
+}
+
+int sage_attn_fwd_sparse(const void* q, const void* k, const void* v, void* o, int B, int H, int N, int d, int mode,
+                         const int32_t* lists, const int32_t* counts, int width, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  const int rc = check_sparse(q, k, v, o, B, H, N, d, mode, lists, counts, width, workspace, workspace_bytes);
+  if (rc != SAGE_OK) return rc;
+  return run_sparse(q, k, v, o, B, H, N, d, mode, lists, counts, width, static_cast<char*>(workspace),
+                    kDefaultTimeoutCycles, 0, static_cast<cudaStream_t>(stream));
+}
+
+int sage_dbg_sparse_forced_timeout(const void* q, const void* k, const void* v, void* o, int B, int H, int N, int d,
+                                   int mode, const int32_t* lists, const int32_t* counts, int width, void* workspace,
+                                   size_t workspace_bytes, long long timeout_cycles, void* stream) {
+  if (timeout_cycles < 1000 || timeout_cycles > kDefaultTimeoutCycles) return SAGE_EINVAL;
+  const int rc = check_sparse(q, k, v, o, B, H, N, d, mode, lists, counts, width, workspace, workspace_bytes);
+  if (rc != SAGE_OK) return rc;
+  return run_sparse(q, k, v, o, B, H, N, d, mode, lists, counts, width, static_cast<char*>(workspace), timeout_cycles,
+                    1, static_cast<cudaStream_t>(stream));
 }
 
 size_t sage_seqpar_workspace_bytes(int P, int B, int Nl, int Hl, int d, int mode) {
@@ -485,8 +653,6 @@ int attn_layer_schedule(int num_layers, const int* full_precision_layers, int n_
 }
 
 namespace {
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
 int check_linear(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, const void* bias, void* y,
                  int y_dtype, int M, int N, int K, void* status) {
   if (M < 1 || N < 128 || K < 128 || N % 128 != 0 || K % 128 != 0) return SAGE_EINVAL;
@@ -628,6 +794,7 @@ int sage_status(void* workspace, void* stream) {
   if (cudaMemsetAsync(workspace, 0, sizeof(word), st) != cudaSuccess) return SAGE_ELAUNCH;
   if (cudaStreamSynchronize(st) != cudaSuccess) return SAGE_ELAUNCH;
   if (word & kStatusTimeout) return SAGE_ETIMEOUT;
+  if (word & kStatusBadIndex) return SAGE_EINVAL;
   return word ? SAGE_ELAUNCH : SAGE_OK;
 }
 

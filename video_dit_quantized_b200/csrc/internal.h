@@ -12,6 +12,7 @@ constexpr int kTile = 128;
 
 // Bits OR-ed into the device status word.
 constexpr uint32_t kStatusTimeout = 1u;
+constexpr uint32_t kStatusBadIndex = 2u;   // a block list held an index or a count out of range
 
 // ---- debug build (-DSAGE_DEBUG): device-side bounds checks ----------------
 // In a debug build every global access of the prepass, the attention
@@ -59,12 +60,18 @@ enum DebugSite : unsigned {
   kSiteQuantIn, kSiteQuantPartials, kSiteQuantK8, kSiteQuantKScale, kSiteQuantV8,
   kSiteAttnQScale = 20, kSiteAttnKScale, kSiteAttnVScale, kSiteAttnOut,
   kSiteUlyssesSrc = 30, kSiteUlyssesDst,
+  kSiteNormIn = 40, kSiteNormTable, kSiteNormOut,
+  kSitePoolIn = 50, kSitePoolOut, kSiteSelectOut,
+  kSiteSparseList = 60, kSiteSparseScale, kSiteSparseOut,
   kSiteSelftest = 99
 };
 // Per translation unit: reads and clears its debug words (0 in a release build).
 unsigned debug_take_prepass(unsigned long long* first);
 unsigned debug_take_attention(unsigned long long* first);
 unsigned debug_take_ulysses(unsigned long long* first);
+unsigned debug_take_norm_rope(unsigned long long* first);
+unsigned debug_take_select(unsigned long long* first);
+unsigned debug_take_sparse(unsigned long long* first);
 // A kernel that fails one check on purpose (the index equals the extent; no
 // memory is touched): the debug path's self-test.
 cudaError_t launch_debug_selftest(cudaStream_t stream);
@@ -132,6 +139,27 @@ cudaError_t launch_linear_bf16(const void* x, const void* w, const void* bias, v
 // Ulysses layout permutations (op 0..3, see ulysses.cu).
 cudaError_t launch_ulysses_permute(const void* src, void* dst, int B, int Nl, int H, int d, int P, int op,
                                    long long chunk_rows, long long base_rows, cudaStream_t stream);
+
+// Norm of queries and keys with the position rotation (q or k may be null; strides in channels).
+cudaError_t launch_qk_norm_rope(const void* q, const void* k, long long q_stride, long long k_stride, const void* wq,
+                                const void* bq, const void* wk, const void* bk, int w_f32, const float* cos_t,
+                                const float* sin_t, int B, int N, int H, int d, int norm, int all_heads, float eps,
+                                int rope, int rope_begin, int rope_len, void* q_out, void* k_out, int ranks,
+                                cudaStream_t stream);
+
+// Key blocks of every query block by pooled scores.
+size_t select_scratch_bytes(int BH, int N, int d);
+cudaError_t launch_select_blocks(const void* q, const void* k, int BH, int N, int d, int keep, int first, int window,
+                                 int* lists, int* counts, void* scratch, cudaStream_t stream);
+
+// Attention over listed blocks: lists [BH, nT, width], counts [BH, nT].
+cudaError_t launch_sparse_i8f8(const int8_t* q_i8, const float* q_scale, const int8_t* k_i8, const float* k_scale,
+                               const uint8_t* v_f8t, const float* v_scale, void* o, int BH, int N, int d,
+                               const int* lists, const int* counts, int width, uint32_t* status,
+                               long long timeout_cycles, int dbg_flags, cudaStream_t stream, bool q_per_token);
+cudaError_t launch_sparse_bf16(const void* q, const void* k, const void* v, void* o, int BH, int N, int d,
+                               const int* lists, const int* counts, int width, uint32_t* status,
+                               long long timeout_cycles, int dbg_flags, cudaStream_t stream);
 
 // Tensor-core throughput probe (kind: kKindF16 / kKindF8F6F4 / kKindI8 of sm100.cuh; n 128 or 256).
 cudaError_t launch_mma_peak(int kind, int n, int iters, long long* cycles, uint32_t* status, int grid,

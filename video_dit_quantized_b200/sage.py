@@ -39,6 +39,7 @@ def load_library(path: str) -> ctypes.CDLL:
         raise ImportError(f"{os.path.basename(path)} is not built ({path}); run video_dit_quantized_b200.build.build()")
     lib = ctypes.CDLL(path)
     vp, i32, sz, ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
+    dbl = ctypes.c_double
     sig = {
         "sage_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
         "sage_prepass_scratch_bytes": (sz, [i32, i32, i32, i32]),
@@ -78,6 +79,13 @@ def load_library(path: str) -> ctypes.CDLL:
         "sage_dbg_bounds_selftest": (i32, [vp]),
         "sage_dbg_mma_peak": (i32, [i32, i32, i32, vp, i32, vp, vp]),
         "sage_dbg_linear_bf16_forced_timeout": (i32, [vp, vp, vp, vp, i32, i32, i32, i32, vp, ll, vp]),
+        # include/sage_sparse.h (wrapped in sparse.py)
+        "sage_qk_norm_rope": (i32, [vp, vp, ll, ll, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, dbl, i32,
+                                    i32, i32, vp, vp, i32, vp]),
+        "sage_select_scratch_bytes": (sz, [i32, i32, i32, i32]),
+        "sage_select_blocks": (i32, [vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, vp, vp, sz, vp]),
+        "sage_attn_fwd_sparse": (i32, [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, vp, sz, vp]),
+        "sage_dbg_sparse_forced_timeout": (i32, [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, vp, sz, ll, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
