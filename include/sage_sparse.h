@@ -103,19 +103,29 @@ int sage_select_blocks(const void* q, const void* k, int B, int H, int N, int d,
  * order; an empty list gives rows of 0.  A block listed twice counts twice.
  * mode as in sage_attn_fwd; in the INT8/FP8 modes the statistics of the prepass
  * (the K mean, the V scales) are those of the whole sequence.  A list of all
- * blocks in ascending order gives the bits of sage_attn_fwd.
+ * blocks in ascending order gives the bits of sage_attn_fwd (with
+ * SAGE_COEFF_DIVIDE).
  *
  * q, k, v, o  bf16 [B, H, N, d]; o must not overlap the other buffers
  * lists     int32 [B, H, nT, width], width >= 1 (sage_select_blocks' keep, or any)
  * counts    int32 [B, H, nT], 0 .. width
+ * coeff     how the INT8/FP8 modes round the quantization coefficients scale =
+ *           amax / top and top / amax (top 127 or 448).  SAGE_COEFF_DIVIDE: correctly
+ *           rounded divisions, the codes of sage_quantize_qk.
+ *           SAGE_COEFF_RECIPROCAL: amax * fl(1 / top) and fl(1 / amax) * top, the
+ *           codes that a torch program gets on the GPU from amax / 127.0 and
+ *           127.0 / amax (a division by a number, or of one, is a product with a
+ *           rounded reciprocal there); a code at a rounding border may differ.
  * workspace as in sage_attn_fwd (sage_workspace_bytes, 256-byte aligned, zero
  *           status word before the first call)
  * The lists are read on the device: an index outside [0, nT) adds nothing, a
  * count outside [0, width] is clamped, and sage_status() on the workspace then
  * returns SAGE_EINVAL.
  */
+#define SAGE_COEFF_DIVIDE 0
+#define SAGE_COEFF_RECIPROCAL 1
 int sage_attn_fwd_sparse(const void* q, const void* k, const void* v, void* o, int B, int H, int N, int d, int mode,
-                         const int32_t* lists, const int32_t* counts, int width, void* workspace,
+                         const int32_t* lists, const int32_t* counts, int width, int coeff, void* workspace,
                          size_t workspace_bytes, void* stream);
 
 /*
@@ -124,8 +134,8 @@ int sage_attn_fwd_sparse(const void* q, const void* k, const void* v, void* o, i
  * records SAGE_ETIMEOUT in the workspace's status word and returns.
  */
 int sage_dbg_sparse_forced_timeout(const void* q, const void* k, const void* v, void* o, int B, int H, int N, int d,
-                                   int mode, const int32_t* lists, const int32_t* counts, int width, void* workspace,
-                                   size_t workspace_bytes, long long timeout_cycles, void* stream);
+                                   int mode, const int32_t* lists, const int32_t* counts, int width, int coeff,
+                                   void* workspace, size_t workspace_bytes, long long timeout_cycles, void* stream);
 
 #ifdef __cplusplus
 }

@@ -202,6 +202,47 @@ def test_bad_indices_and_counts_are_reported_and_skipped(mode, cuda_dev):
     assert sage.status(ws) == sage.OK and torch.equal(bits(again), bits(ref))
 
 
+@pytest.mark.parametrize("mode", [I8, QTOK])
+@pytest.mark.parametrize("d", [64, 128])
+def test_reciprocal_coefficients_are_torch_codes(mode, d, cuda_dev):
+    """COEFF_RECIPROCAL: the workspace holds the codes and scales of torch's `127.0 / amax` and `amax / 127.0` on the
+    GPU, bit for bit; COEFF_DIVIDE holds those of sage_quantize_qk."""
+    from video_dit_quantized_b200 import sage, sparse
+    B, H, N = 1, 3, 3000
+    nT, G = 24, 3
+    q, k, v, g = inputs(B, H, N, d, 70, cuda_dev)
+    v[0, 1, :, 3] = 0
+    k[0, 2] = k[0, 2, :1]                                             # smoothed to zero: scale 0
+    lists, counts = random_lists(B, H, nT, 3, g, cuda_dev, lo=1)
+    size = {"q_i8": G * nT * 128 * d, "k_i8": G * nT * 128 * d, "v_f8t": G * nT * 128 * d,
+            "q_scale": 4 * G * (nT * 128 if mode == QTOK else nT), "k_scale": 4 * G * nT, "k_mean": 4 * G * d,
+            "v_scale": 4 * G * d}
+    pad = lambda x: torch.nn.functional.pad(x.float().view(G, N, d), (0, 0, 0, nT * 128 - N)).view(G, nT, 128, d)
+    mean = (k.double().sum(2, keepdim=True) / torch.full((), N, dtype=torch.float64, device=cuda_dev)).float()
+    vmax = v.float().abs().amax(2).view(G, d)
+    want = {"k_mean": mean.flatten(), "v_scale": (vmax / 448.0).flatten()}
+    inv = torch.where(vmax > 0, 448.0 / vmax, 0.0)
+    want["v_f8t"] = (pad(v) * inv[:, None, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8).view(
+        G, nT * 128, d).transpose(1, 2).flatten()
+    for name, x, dims in (("q", pad(q), (3,) if mode == QTOK else (2, 3)), ("k", pad(k.float() - mean), (2, 3))):
+        if name == "k":
+            x[:, -1, N - (nT - 1) * 128:] = 0
+        amax = x.abs().amax(dims, keepdim=True)
+        want[name + "_scale"] = (amax / 127.0).flatten()
+        want[name + "_i8"] = (x * torch.where(amax > 0, 127.0 / amax, 0.0)).round().clamp(-127, 127).to(torch.int8).flatten()
+    for coeff in (sparse.COEFF_RECIPROCAL, sparse.COEFF_DIVIDE):
+        ws = sage.alloc_workspace(B, H, N, d, mode, cuda_dev)
+        sparse.attn_fwd_sparse(q, k, v, mode, lists, counts, coeff=coeff, workspace=ws)
+        if coeff == sparse.COEFF_DIVIDE:
+            pre = sage.quantize_qk(q, k, v, q_per_token=mode == QTOK)
+            want = {n: pre[n].flatten() for n in size}
+        at = 256
+        for name, n in size.items():
+            got = ws[at:at + n]
+            assert torch.equal(got, want[name].contiguous().view(torch.uint8)), (name, coeff)
+            at += -(-n // 256) * 256
+
+
 def test_blocks_that_are_not_listed_are_not_touched(cuda_dev):
     """BF16: NaN and infinity in keys and values of other blocks change nothing (no statistics cross blocks)."""
     from video_dit_quantized_b200 import sparse

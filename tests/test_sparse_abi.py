@@ -36,7 +36,7 @@ def test_header_constants_match_the_binding():
     txt = open(sparse.HEADER).read()
     value = lambda n: int(re.search(rf"#define SAGE_{n} (\d+)", txt).group(1))
     for name in ("NORM_NONE", "NORM_RMS", "NORM_LAYER", "NORM_SCOPE_HEAD", "NORM_SCOPE_ALL", "ROPE_NONE",
-                 "ROPE_INTERLEAVED", "ROPE_HALF", "NORM_MAX_WIDTH", "SELECT_MAX_BLOCKS"):
+                 "ROPE_INTERLEAVED", "ROPE_HALF", "COEFF_DIVIDE", "COEFF_RECIPROCAL", "NORM_MAX_WIDTH", "SELECT_MAX_BLOCKS"):
         assert value(name) == getattr(sparse, name), name
 
 
@@ -106,9 +106,9 @@ def test_select_refusals():
 def test_sparse_refusals():
     n = sage.workspace_bytes(1, 2, 1000, 128, sage.MODE_INT8_FP8)
     base = dict(q=1 << 30, k=2 << 30, v=3 << 30, o=4 << 30, B=1, H=2, N=1000, d=128, mode=1, li=5 << 30, co=6 << 30,
-                width=3, ws=7 << 30, nb=n)
+                width=3, coeff=0, ws=7 << 30, nb=n)
     call = lambda **kw: sage.LIB.sage_attn_fwd_sparse(*{**base, **kw}.values(), None)
-    for kw in (dict(q=None), dict(v=(3 << 30) + 8), dict(N=0), dict(mode=3), dict(mode=-1), dict(width=0), dict(li=None),
+    for kw in (dict(q=None), dict(v=(3 << 30) + 8), dict(N=0), dict(mode=3), dict(mode=-1), dict(width=0), dict(coeff=2), dict(coeff=-1), dict(li=None),
                dict(co=(6 << 30) + 2), dict(ws=(7 << 30) + 16), dict(o=1 << 30), dict(o=(2 << 30) + 1024),
                dict(o=5 << 30), dict(o=6 << 30), dict(o=7 << 30), dict(H=70000)):
         assert call(**kw) == sage.EINVAL, kw

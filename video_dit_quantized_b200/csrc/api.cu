@@ -351,11 +351,12 @@ int check_norm_tensor(const void* x, long long stride, const void* w, const void
 }
 
 int check_sparse(const void* q, const void* k, const void* v, void* o, int B, int H, int N, int d, int mode,
-                 const int32_t* lists, const int32_t* counts, int width, void* workspace, size_t workspace_bytes) {
+                 const int32_t* lists, const int32_t* counts, int width, int coeff, void* workspace,
+                 size_t workspace_bytes) {
   const int rc = check_shape(B, H, N, d);
   if (rc != SAGE_OK) return rc;
   if (mode != SAGE_MODE_BF16 && mode != SAGE_MODE_INT8_FP8 && mode != SAGE_MODE_INT8_FP8_QTOKEN) return SAGE_EINVAL;
-  if (width < 1) return SAGE_EINVAL;
+  if (width < 1 || (coeff != SAGE_COEFF_DIVIDE && coeff != SAGE_COEFF_RECIPROCAL)) return SAGE_EINVAL;
   const void* ptrs[] = {q, k, v, o, workspace};
   for (const void* p : ptrs)
     if (!p || !aligned16(p)) return SAGE_EINVAL;
@@ -371,8 +372,8 @@ int check_sparse(const void* q, const void* k, const void* v, void* o, int B, in
 }
 
 int run_sparse(const void* q, const void* k, const void* v, void* o, int B, int H, int N, int d, int mode,
-               const int32_t* lists, const int32_t* counts, int width, char* ws, long long timeout_cycles,
-               int dbg_flags, cudaStream_t st) {
+               const int32_t* lists, const int32_t* counts, int width, int coeff, char* ws,
+               long long timeout_cycles, int dbg_flags, cudaStream_t st) {
   uint32_t* status = reinterpret_cast<uint32_t*>(ws);
   if (mode == SAGE_MODE_BF16)
     return debug_collect(st, launch_status(launch_sparse_bf16(q, k, v, o, B * H, N, d, lists, counts, width, status,
@@ -381,7 +382,8 @@ int run_sparse(const void* q, const void* k, const void* v, void* o, int B, int 
   const Operands op(ws, B, H, N, d, qtok);
   const RowMap plain{0, 0, 0, 0};
   const cudaError_t e = launch_prepass(q, k, v, B * H, N, d, op.q_i8, op.q_scale, op.k_i8, op.k_scale, op.k_mean,
-                                       op.v_f8t, op.v_scale, op.scratch, st, qtok, plain);
+                                       op.v_f8t, op.v_scale, op.scratch, st, qtok, plain,
+                                       coeff == SAGE_COEFF_RECIPROCAL);
   if (e != cudaSuccess) return launch_status(e);
   return debug_collect(st, launch_status(launch_sparse_i8f8(op.q_i8, op.q_scale, op.k_i8, op.k_scale, op.v_f8t,
                                                             op.v_scale, o, B * H, N, d, lists, counts, width, status,
@@ -465,21 +467,21 @@ int sage_select_blocks(const void* q, const void* k, int B, int H, int N, int d,
 }
 
 int sage_attn_fwd_sparse(const void* q, const void* k, const void* v, void* o, int B, int H, int N, int d, int mode,
-                         const int32_t* lists, const int32_t* counts, int width, void* workspace,
+                         const int32_t* lists, const int32_t* counts, int width, int coeff, void* workspace,
                          size_t workspace_bytes, void* stream) {
-  const int rc = check_sparse(q, k, v, o, B, H, N, d, mode, lists, counts, width, workspace, workspace_bytes);
+  const int rc = check_sparse(q, k, v, o, B, H, N, d, mode, lists, counts, width, coeff, workspace, workspace_bytes);
   if (rc != SAGE_OK) return rc;
-  return run_sparse(q, k, v, o, B, H, N, d, mode, lists, counts, width, static_cast<char*>(workspace),
+  return run_sparse(q, k, v, o, B, H, N, d, mode, lists, counts, width, coeff, static_cast<char*>(workspace),
                     kDefaultTimeoutCycles, 0, static_cast<cudaStream_t>(stream));
 }
 
 int sage_dbg_sparse_forced_timeout(const void* q, const void* k, const void* v, void* o, int B, int H, int N, int d,
-                                   int mode, const int32_t* lists, const int32_t* counts, int width, void* workspace,
-                                   size_t workspace_bytes, long long timeout_cycles, void* stream) {
+                                   int mode, const int32_t* lists, const int32_t* counts, int width, int coeff,
+                                   void* workspace, size_t workspace_bytes, long long timeout_cycles, void* stream) {
   if (timeout_cycles < 1000 || timeout_cycles > kDefaultTimeoutCycles) return SAGE_EINVAL;
-  const int rc = check_sparse(q, k, v, o, B, H, N, d, mode, lists, counts, width, workspace, workspace_bytes);
+  const int rc = check_sparse(q, k, v, o, B, H, N, d, mode, lists, counts, width, coeff, workspace, workspace_bytes);
   if (rc != SAGE_OK) return rc;
-  return run_sparse(q, k, v, o, B, H, N, d, mode, lists, counts, width, static_cast<char*>(workspace), timeout_cycles,
+  return run_sparse(q, k, v, o, B, H, N, d, mode, lists, counts, width, coeff, static_cast<char*>(workspace), timeout_cycles,
                     1, static_cast<cudaStream_t>(stream));
 }
 

@@ -109,11 +109,12 @@ size_t prepass_scratch_bytes(int BH, int N, int d);
 PrepassScratch prepass_scratch_carve(void* base, int BH, int N, int d);
 
 // q_per_token: q_scale is [BH, Npad] (one scale per token) instead of [BH, nT].
-// in_map: where token n of head bh sits in q, k and v.
+// in_map: where token n of head bh sits in q, k and v.  recip: the coefficients
+// by multiplication with rounded reciprocals instead of by division.
 cudaError_t launch_prepass(const void* q, const void* k, const void* v, int BH, int N, int d, int8_t* q_i8,
                            float* q_scale, int8_t* k_i8, float* k_scale, float* k_mean, uint8_t* v_f8t,
                            float* v_scale, const PrepassScratch& scratch, cudaStream_t stream,
-                           bool q_per_token = false, RowMap in_map = RowMap{0, 0, 0, 0});
+                           bool q_per_token = false, RowMap in_map = RowMap{0, 0, 0, 0}, bool recip = false);
 
 // Quantized attention (INT8 QK^T, FP8 PV).  status: device uint32 word.
 cudaError_t launch_attn_i8f8(const int8_t* q_i8, const float* q_scale, const int8_t* k_i8, const float* k_scale,

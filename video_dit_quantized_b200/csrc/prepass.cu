@@ -36,6 +36,18 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
   x[6] = bf16_lo(u.w); x[7] = bf16_hi(u.w);
 }
 
+// The coefficients of one block or channel, 0 where amax is 0: scale = amax / top
+// and its inverse top / amax, each a correctly rounded division, or (recip) a
+// product with a rounded reciprocal, which may differ in the last bit.
+__device__ __forceinline__ float coef_scale(float amax, float top, bool recip) {
+  if (!(amax > 0.f)) return 0.f;
+  return recip ? __fmul_rn(amax, __frcp_rn(top)) : __fdiv_rn(amax, top);
+}
+__device__ __forceinline__ float coef_inv(float top, float amax, bool recip) {
+  if (!(amax > 0.f)) return 0.f;
+  return recip ? __fmul_rn(__frcp_rn(amax), top) : __fdiv_rn(top, amax);
+}
+
 __device__ __forceinline__ int quant_i8(float x, float inv) {
   int c = __float2int_rn(__fmul_rn(x, inv));
   return max(-127, min(127, c));
@@ -69,7 +81,7 @@ __global__ void __launch_bounds__(kThreads, 3) prepass_stats_kernel(const uint4*
                                                                  const uint4* __restrict__ v, int N, int Npad,
                                                                  int8_t* __restrict__ q_i8,
                                                                  float* __restrict__ q_scale, PrepassScratch scr,
-                                                                 RowMap in_map) {
+                                                                 RowMap in_map, bool recip) {
   constexpr int V8 = D / 8;                        // uint4 per token row
   constexpr int PER_T = kTile * V8 / kThreads;     // uint4 per thread per block
   static_assert(kThreads % V8 == 0, "a thread must always see the same 8 channels");
@@ -127,9 +139,9 @@ __global__ void __launch_bounds__(kThreads, 3) prepass_stats_kernel(const uint4*
   }
   uint2* qo = reinterpret_cast<uint2*>(q_i8 + ((size_t)bh * Npad + n0) * D);
   if constexpr (!TOKQ) {
-    const float qinv = amax > 0.f ? __fdiv_rn(127.0f, amax) : 0.f;
+    const float qinv = coef_inv(127.0f, amax, recip);
     if (threadIdx.x == 0 && SAGE_DCHECK((size_t)bh * nK + kb, BHt * nK, kSiteStatsQScale))
-      q_scale[(size_t)bh * nK + kb] = amax > 0.f ? __fdiv_rn(amax, 127.0f) : 0.f;
+      q_scale[(size_t)bh * nK + kb] = coef_scale(amax, 127.0f, recip);
 #pragma unroll
     for (int i = 0; i < PER_T; ++i) {
       const int e = threadIdx.x + i * kThreads;
@@ -153,9 +165,9 @@ __global__ void __launch_bounds__(kThreads, 3) prepass_stats_kernel(const uint4*
       for (int u = 0; u < 8; ++u) ra = fmaxf(ra, fabsf(x[u]));
 #pragma unroll
       for (int o = V8 / 2; o > 0; o >>= 1) ra = fmaxf(ra, __shfl_xor_sync(0xffffffffu, ra, o));
-      const float rinv = ra > 0.f ? __fdiv_rn(127.0f, ra) : 0.f;
+      const float rinv = coef_inv(127.0f, ra, recip);
       if (e % V8 == 0 && SAGE_DCHECK((size_t)bh * Npad + n0 + e / V8, BHt * Npad, kSiteStatsQScale))
-        q_scale[(size_t)bh * Npad + n0 + e / V8] = ra > 0.f ? __fdiv_rn(ra, 127.0f) : 0.f;
+        q_scale[(size_t)bh * Npad + n0 + e / V8] = coef_scale(ra, 127.0f, recip);
       int c[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) c[u] = rinv > 0.f ? quant_i8(x[u], rinv) : 0;
@@ -198,7 +210,7 @@ constexpr int kFinBatch = 32;
 template <int D>
 __global__ void __launch_bounds__(64) prepass_finalize_kernel(int N, int nK, PrepassScratch scr,
                                                               float* __restrict__ k_mean,
-                                                              float* __restrict__ v_scale) {
+                                                              float* __restrict__ v_scale, bool recip) {
   const int bh = blockIdx.x;
   const int c = blockIdx.y * 32 + (threadIdx.x & 31);
   const size_t col = (size_t)bh * nK * D + c;       // partial (bh, block 0, c); block t is t * D further
@@ -250,7 +262,7 @@ __global__ void __launch_bounds__(64) prepass_finalize_kernel(int N, int nK, Pre
       take(B);
     }
     if (SAGE_DCHECK((size_t)bh * D + c, out_ext, kSiteFinOut)) {
-      v_scale[(size_t)bh * D + c] = a > 0.f ? __fdiv_rn(a, 448.0f) : 0.f;
+      v_scale[(size_t)bh * D + c] = coef_scale(a, 448.0f, recip);
       scr.v_amax[(size_t)bh * D + c] = a;
     }
   }
@@ -264,7 +276,7 @@ __global__ void __launch_bounds__(kThreads) prepass_quant_kv_kernel(const uint4*
                                                                     int8_t* __restrict__ k_i8,
                                                                     float* __restrict__ k_scale,
                                                                     uint8_t* __restrict__ v_f8t, PrepassScratch scr,
-                                                                    RowMap in_map) {
+                                                                    RowMap in_map, bool recip) {
   constexpr int V8 = D / 8;
   constexpr int PER_T = kTile * V8 / kThreads;
   __shared__ float mean_s[D];
@@ -317,12 +329,12 @@ __global__ void __launch_bounds__(kThreads) prepass_quant_kv_kernel(const uint4*
     mean_s[c] = m;
     if (SAGE_DCHECK(pidx + c, part_ext, kSiteQuantPartials))
       kam = fmaxf(fabsf(__fsub_rn(scr.k_pmax[pidx + c], m)), fabsf(__fsub_rn(scr.k_pmin[pidx + c], m)));
-    vinv_s[c] = a > 0.f ? __fdiv_rn(448.0f, a) : 0.f;
+    vinv_s[c] = coef_inv(448.0f, a, recip);
   }
   kam = block_max(kam, red);   // contains __syncthreads
-  const float kinv = kam > 0.f ? __fdiv_rn(127.0f, kam) : 0.f;
+  const float kinv = coef_inv(127.0f, kam, recip);
   if (threadIdx.x == 0 && SAGE_DCHECK((size_t)bh * nK + kb, BHt * nK, kSiteQuantKScale))
-    k_scale[(size_t)bh * nK + kb] = kam > 0.f ? __fdiv_rn(kam, 127.0f) : 0.f;
+    k_scale[(size_t)bh * nK + kb] = coef_scale(kam, 127.0f, recip);
 
   // ---- K: smoothed INT8 codes ----
   uint2* ko = reinterpret_cast<uint2*>(k_i8 + ((size_t)bh * Npad + n0) * D);
@@ -373,7 +385,7 @@ template <int D>
 cudaError_t launch_prepass_d(const void* q, const void* k, const void* v, int BH, int N, int8_t* q_i8,
                              float* q_scale, int8_t* k_i8, float* k_scale, float* k_mean, uint8_t* v_f8t,
                              float* v_scale, const PrepassScratch& scr, bool q_per_token, cudaStream_t stream,
-                             RowMap in_map) {
+                             RowMap in_map, bool recip) {
   const int nK = num_tiles(N), Npad = nK * kTile;
   const bool chunked = in_map.P != 0;
   if (chunked && in_map.B * in_map.Hl != BH) return cudaErrorInvalidValue;
@@ -382,20 +394,24 @@ cudaError_t launch_prepass_d(const void* q, const void* k, const void* v, int BH
   const uint4* k4 = static_cast<const uint4*>(k);
   const uint4* v4 = static_cast<const uint4*>(v);
   if (q_per_token && chunked)
-    prepass_stats_kernel<D, true, true><<<grid, kThreads, 0, stream>>>(q4, k4, v4, N, Npad, q_i8, q_scale, scr, in_map);
+    prepass_stats_kernel<D, true, true><<<grid, kThreads, 0, stream>>>(q4, k4, v4, N, Npad, q_i8, q_scale, scr, in_map,
+                                                                         recip);
   else if (q_per_token)
-    prepass_stats_kernel<D, true, false><<<grid, kThreads, 0, stream>>>(q4, k4, v4, N, Npad, q_i8, q_scale, scr, in_map);
+    prepass_stats_kernel<D, true, false><<<grid, kThreads, 0, stream>>>(q4, k4, v4, N, Npad, q_i8, q_scale, scr, in_map,
+                                                                         recip);
   else if (chunked)
-    prepass_stats_kernel<D, false, true><<<grid, kThreads, 0, stream>>>(q4, k4, v4, N, Npad, q_i8, q_scale, scr, in_map);
+    prepass_stats_kernel<D, false, true><<<grid, kThreads, 0, stream>>>(q4, k4, v4, N, Npad, q_i8, q_scale, scr, in_map,
+                                                                         recip);
   else
-    prepass_stats_kernel<D, false, false><<<grid, kThreads, 0, stream>>>(q4, k4, v4, N, Npad, q_i8, q_scale, scr, in_map);
-  prepass_finalize_kernel<D><<<dim3(BH, D / 32), 64, 0, stream>>>(N, nK, scr, k_mean, v_scale);
+    prepass_stats_kernel<D, false, false><<<grid, kThreads, 0, stream>>>(q4, k4, v4, N, Npad, q_i8, q_scale, scr, in_map,
+                                                                         recip);
+  prepass_finalize_kernel<D><<<dim3(BH, D / 32), 64, 0, stream>>>(N, nK, scr, k_mean, v_scale, recip);
   if (chunked)
     prepass_quant_kv_kernel<D, true><<<grid, kThreads, 0, stream>>>(k4, v4, N, Npad, k_mean, k_i8, k_scale, v_f8t, scr,
-                                                                    in_map);
+                                                                    in_map, recip);
   else
     prepass_quant_kv_kernel<D, false><<<grid, kThreads, 0, stream>>>(k4, v4, N, Npad, k_mean, k_i8, k_scale, v_f8t, scr,
-                                                                     in_map);
+                                                                     in_map, recip);
   return cudaGetLastError();
 }
 
@@ -444,13 +460,13 @@ PrepassScratch prepass_scratch_carve(void* base, int BH, int N, int d) {
 cudaError_t launch_prepass(const void* q, const void* k, const void* v, int BH, int N, int d, int8_t* q_i8,
                            float* q_scale, int8_t* k_i8, float* k_scale, float* k_mean, uint8_t* v_f8t,
                            float* v_scale, const PrepassScratch& scratch, cudaStream_t stream, bool q_per_token,
-                           RowMap in_map) {
+                           RowMap in_map, bool recip) {
   if (d == 128)
     return launch_prepass_d<128>(q, k, v, BH, N, q_i8, q_scale, k_i8, k_scale, k_mean, v_f8t, v_scale, scratch,
-                                 q_per_token, stream, in_map);
+                                 q_per_token, stream, in_map, recip);
   if (d == 64)
     return launch_prepass_d<64>(q, k, v, BH, N, q_i8, q_scale, k_i8, k_scale, k_mean, v_f8t, v_scale, scratch,
-                                q_per_token, stream, in_map);
+                                q_per_token, stream, in_map, recip);
   return cudaErrorInvalidValue;
 }
 

@@ -84,8 +84,9 @@ def load_library(path: str) -> ctypes.CDLL:
                                     i32, i32, vp, vp, i32, vp]),
         "sage_select_scratch_bytes": (sz, [i32, i32, i32, i32]),
         "sage_select_blocks": (i32, [vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, vp, vp, sz, vp]),
-        "sage_attn_fwd_sparse": (i32, [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, vp, sz, vp]),
-        "sage_dbg_sparse_forced_timeout": (i32, [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, vp, sz, ll, vp]),
+        "sage_attn_fwd_sparse": (i32, [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, i32, vp, sz, vp]),
+        "sage_dbg_sparse_forced_timeout": (i32, [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, i32, vp, sz, ll,
+                                                 vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)

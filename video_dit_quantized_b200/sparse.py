@@ -21,6 +21,7 @@ from .sage import BLK, EINVAL, SageError, _check, _need
 NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
 NORM_SCOPE_HEAD, NORM_SCOPE_ALL = 0, 1
 ROPE_NONE, ROPE_INTERLEAVED, ROPE_HALF = 0, 1, 2
+COEFF_DIVIDE, COEFF_RECIPROCAL = 0, 1
 NORM_MAX_WIDTH = 16384
 SELECT_MAX_BLOCKS = 6016
 
@@ -213,11 +214,12 @@ def _sparse_args(q, k, v, o, lists, counts, workspace):
     return B, H, N, d
 
 
-def attn_fwd_sparse(q, k, v, mode: int, lists, counts, o=None, workspace=None, stream=None):
+def attn_fwd_sparse(q, k, v, mode: int, lists, counts, coeff: int = COEFF_DIVIDE, o=None, workspace=None, stream=None):
     """Attention over the listed key blocks through sage_attn_fwd_sparse; returns bf16 O [B, H, N, d].
 
     lists int32 [B, H, nT, width], counts int32 [B, H, nT] as select_blocks gives them, or any lists: an empty
-    one gives rows of 0.  workspace: sage.alloc_workspace(B, H, N, d, mode); sage.status() on it reports a bad
+    one gives rows of 0.  coeff: how the INT8/FP8 modes round the quantization coefficients, COEFF_DIVIDE (the
+    codes of the dense call) or COEFF_RECIPROCAL (the codes of torch's 127.0 / amax on the GPU).  workspace: sage.alloc_workspace(B, H, N, d, mode); sage.status() on it reports a bad
     index or count (EINVAL).
     """
     import torch
@@ -232,7 +234,7 @@ def attn_fwd_sparse(q, k, v, mode: int, lists, counts, o=None, workspace=None, s
                 raise SageError(EINVAL, "sage_workspace_bytes")
             workspace = call.new(n, torch.uint8, zero=True)
         _check(sage.LIB.sage_attn_fwd_sparse(_p(q), _p(k), _p(v), _p(o), B, H, N, d, int(mode), _p(lists), _p(counts),
-                                             lists.shape[3], _p(workspace),
+                                             lists.shape[3], int(coeff), _p(workspace),
                                              workspace.numel() * workspace.element_size(), call.handle),
                "sage_attn_fwd_sparse")
     return o
@@ -245,7 +247,7 @@ def dbg_sparse_forced_timeout(q, k, v, mode: int, lists, counts, workspace, time
                         ("workspace", workspace))) as call:
         o = call.new((B, H, N, d), torch.bfloat16)
         _check(sage.LIB.sage_dbg_sparse_forced_timeout(_p(q), _p(k), _p(v), _p(o), B, H, N, d, int(mode), _p(lists),
-                                                       _p(counts), lists.shape[3], _p(workspace),
+                                                       _p(counts), lists.shape[3], COEFF_DIVIDE, _p(workspace),
                                                        workspace.numel() * workspace.element_size(),
                                                        int(timeout_cycles), call.handle),
                "sage_dbg_sparse_forced_timeout")
