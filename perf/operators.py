@@ -227,7 +227,7 @@ def _run_own(state, case, op):
                                              scratch=state["scratch"])
         return [lists, counts]
     return sparse.attn_fwd_sparse(state["q"], state["k"], state["v"], state["mode"], state["lists"], state["counts"],
-                                  o=state["o"], workspace=state["workspace"])
+                                  coeff=sparse.COEFF_RECIPROCAL, o=state["o"], workspace=state["workspace"])
 
 
 # ------------------------------------------------------------------------------------------------ plain forms
