@@ -55,8 +55,8 @@ extern "C" {
  *           An output must not overlap an input or the other output, except
  *           q_out == q (k_out == k) with out_ranks 1 and stride H * d: in place.
  *
- * Arithmetic in fp32, one rounding to bf16.  d 64 or 128, H * d <= 16384, B * N
- * < 2^31.  Errors: SAGE_EINVAL (sizes, strides, pointers, overlap, arguments that do
+ * Arithmetic in fp32, one rounding to bf16.  d 64 or 128, H * d <= 16384, B <=
+ * 65535, B * N < 2^31.  Errors: SAGE_EINVAL (sizes, strides, pointers, overlap, arguments that do
  * not belong together), SAGE_EUNSUPPORTED (d, H * d, device).
  */
 #define SAGE_NORM_NONE 0

@@ -396,7 +396,7 @@ int sage_qk_norm_rope(const void* q, const void* k, long long q_stride, long lon
                       const void* bq, const void* wk, const void* bk, int w_dtype, const float* cos, const float* sin,
                       int B, int N, int H, int d, int norm, int scope, double eps, int rope, int rope_begin,
                       int rope_len, void* q_out, void* k_out, int out_ranks, void* stream) {
-  if (B < 1 || H < 1 || N < 1 || (long long)B * N >= (1LL << 31)) return SAGE_EINVAL;
+  if (B < 1 || B > 65535 || H < 1 || N < 1 || (long long)B * N >= (1LL << 31)) return SAGE_EINVAL;   // grid.z limit
   if (d != 64 && d != 128) return SAGE_EUNSUPPORTED;
   if (H > SAGE_NORM_MAX_WIDTH / d) return SAGE_EUNSUPPORTED;
   if (norm < SAGE_NORM_NONE || norm > SAGE_NORM_LAYER || scope < SAGE_NORM_SCOPE_HEAD || scope > SAGE_NORM_SCOPE_ALL ||

@@ -17,6 +17,11 @@
 // norm over all heads needs no second read.  TPT threads own one token, each
 // CH chunks of eight channels, TPT chunks apart, so a thread always sees the
 // same channels of a head: its cos and sin values are read once a token.
+// Instructions come next: at 24 an element (norm, weights and rotation as
+// run-time choices inside the element loop, 64-bit token arithmetic) the kernel
+// was issue bound, 4.3 TB/s at 1 x 75600 x 40 x 128; hence the scope and the
+// pairing as template arguments, one form (x * r + t) * w for both norms in packed
+// pairs, and one block per token with no division.
 #include <cuda_bf16.h>
 #include <cstdint>
 
@@ -42,28 +47,27 @@ struct NrParams {
   NrTensor t[2];
   const float4* cos4;
   const float4* sin4;
-  long long tokens;      // B * N
-  int N, B, H, norm, all_heads, w_f32, rope, begin, len, ranks;
+  int B, N, H, norm, w_f32, begin, len, ranks;   // len 0: no rotation
+  uint32_t rank_mul;     // ceil(2^16 / heads of a rank): h * rank_mul >> 16 = h / heads of a rank for h < 256
   float eps;
 };
 
-__device__ __forceinline__ void nr_unpack(const uint4& u, float (&x)[8]) {
+__device__ __forceinline__ void nr_unpack(const uint4& u, float2 (&x)[4]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
 
 // eight consecutive weights at vector index i
-__device__ __forceinline__ void nr_weights(const void* w, int w_f32, int i, float (&x)[8]) {
+__device__ __forceinline__ void nr_weights(const void* w, int w_f32, int i, float2 (&x)[4]) {
   if (w_f32) {
-    const float4 a = static_cast<const float4*>(w)[2 * i], b = static_cast<const float4*>(w)[2 * i + 1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    const float4 a = __ldg(static_cast<const float4*>(w) + 2 * i), b = __ldg(static_cast<const float4*>(w) + 2 * i + 1);
+    x[0] = make_float2(a.x, a.y);
+    x[1] = make_float2(a.z, a.w);
+    x[2] = make_float2(b.x, b.y);
+    x[3] = make_float2(b.z, b.w);
   } else {
-    nr_unpack(static_cast<const uint4*>(w)[i], x);
+    nr_unpack(__ldg(static_cast<const uint4*>(w) + i), x);
   }
 }
 
@@ -94,160 +98,173 @@ __device__ __forceinline__ float head_sum(float v) {
 
 __device__ __forceinline__ float inv_root(float v) { return v == 0.f ? 0.f : rsqrtf(v); }
 
-// grid (ceil(tokens / (kNrThreads / TPT)), 2): y selects the tensor.
-template <int D, int TPT, int CH>
+// grid (ceil(N / TOKENS), tensors, B), TOKENS = kNrThreads / TPT
+template <int D, int TPT, int CH, bool ALL, bool HALF>
 __global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(const NrParams p, int first) {
   constexpr int L = D / 8;                 // lanes of one head
+  constexpr int TOKENS = kNrThreads / TPT;
+  constexpr int F = HALF ? 2 : 1;          // float4 of factors a thread needs: 8 pairs (halves) or 4
   static_assert(TPT % L == 0 && kNrThreads % TPT == 0, "a thread must see the same channels in every chunk");
   __shared__ float red[kNrThreads / 32];
-  const long long tok = (long long)blockIdx.x * (kNrThreads / TPT) + threadIdx.x / TPT;
-  if (tok >= p.tokens) return;             // whole warps leave together, and at TPT == 128 the whole block
+  const int b = blockIdx.z, n = blockIdx.x * TOKENS + threadIdx.x / TPT;
+  if (n >= p.N) return;                    // whole warps leave together, and at TPT == 128 the whole block
   const NrTensor t = p.t[first + blockIdx.y];
   const int lane = threadIdx.x % TPT;
+  const int l = lane % L;
   const int nvec = p.H * L;
-  const int b = (int)(tok / p.N), n = (int)(tok - (long long)b * p.N);
-  const uint4* row = t.x + tok * t.stride8;
+  const long long tokens = (long long)p.B * p.N, tok = (long long)b * p.N + n;
+  (void)tokens;
 
-  uint4 raw[CH];
+  float2 x[CH][4];
+  const uint4* row = t.x + tok * t.stride8 + lane;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = i * TPT + lane;
-    raw[i] = make_uint4(0, 0, 0, 0);
-    if (c < nvec && SAGE_DCHECK(tok * t.stride8 + c, (p.tokens - 1) * t.stride8 + nvec, kSiteNormIn)) raw[i] = row[c];
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (i * TPT + lane < nvec && SAGE_DCHECK(tok * t.stride8 + i * TPT + lane, (tokens - 1) * t.stride8 + nvec, kSiteNormIn))
+      u = row[i * TPT];
+    nr_unpack(u, x[i]);
   }
-
-  // this thread's rotation factors: 4 pairs (interleaved) or 8 (halves)
-  const int l = lane % L;
-  const bool turn = p.rope != SAGE_ROPE_NONE && n >= p.begin && n - p.begin < p.len;
-  float cs[8], sn[8];
+  // this thread's rotation factors
+  const int at = n - p.begin;
+  const bool turn = at >= 0 && at < p.len;
+  float cs[4 * F], sn[4 * F];
   if (turn) {
-    const long long base = (long long)(n - p.begin) * (D / 8);   // in float4: d / 2 floats a row
-    if (SAGE_DCHECK(base + D / 8 - 1, (long long)p.len * (D / 8), kSiteNormTable)) {
-      const int i0 = p.rope == SAGE_ROPE_INTERLEAVED ? l : 2 * (l % (L / 2));
-      const float4 c0 = p.cos4[base + i0], s0 = p.sin4[base + i0];
-      cs[0] = c0.x; cs[1] = c0.y; cs[2] = c0.z; cs[3] = c0.w;
-      sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w;
-      if (p.rope == SAGE_ROPE_HALF) {
-        const float4 c1 = p.cos4[base + i0 + 1], s1 = p.sin4[base + i0 + 1];
-        cs[4] = c1.x; cs[5] = c1.y; cs[6] = c1.z; cs[7] = c1.w;
-        sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
+    const long long base = (long long)at * (D / 8) + (HALF ? 2 * (l % (L / 2)) : l);   // in float4: d / 2 floats a row
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+      if (SAGE_DCHECK(base + f, (long long)p.len * (D / 8), kSiteNormTable)) {
+        const float4 c4 = __ldg(p.cos4 + base + f), s4 = __ldg(p.sin4 + base + f);
+        cs[4 * f] = c4.x; cs[4 * f + 1] = c4.y; cs[4 * f + 2] = c4.z; cs[4 * f + 3] = c4.w;
+        sn[4 * f] = s4.x; sn[4 * f + 1] = s4.y; sn[4 * f + 2] = s4.z; sn[4 * f + 3] = s4.w;
       }
-    }
+  }
+  float2 wv[4], bv[4];
+  if (!ALL) {
+    if (t.w) nr_weights(t.w, p.w_f32, l, wv);
+    if (t.b) nr_weights(t.b, p.w_f32, l, bv);
   }
 
-  float mu = 0.f, r = 1.f;                 // statistics over all heads
-  if (p.norm != SAGE_NORM_NONE && p.all_heads) {
-    const float cnt = (float)(p.H * D);
+  // y = x * r + shift before the weights
+  float r = 1.f, shift = 0.f;
+  if (ALL && p.norm != SAGE_NORM_NONE) {
+    const float inv = 1.f / (float)(p.H * D);
+    float mu = 0.f;
     if (p.norm == SAGE_NORM_LAYER) {
-      float s = 0.f;
+      float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        float x[8];
-        nr_unpack(raw[i], x);
+      for (int i = 0; i < CH; ++i)
 #pragma unroll
-        for (int u = 0; u < 8; ++u) s += x[u];
-      }
-      mu = token_sum<TPT>(s, red) / cnt;
+        for (int u = 0; u < 4; ++u) s = fadd2(s, x[i][u]);
+      mu = token_sum<TPT>(s.x + s.y, red) * inv;
     }
-    float s = 0.f;
+    float2 s = make_float2(0.f, 0.f);
+    const float2 m2 = make_float2(mu, mu);
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      float x[8];
-      nr_unpack(raw[i], x);
+    for (int i = 0; i < CH; ++i)
       if (i * TPT + lane < nvec)
 #pragma unroll
-        for (int u = 0; u < 8; ++u) s += (x[u] - mu) * (x[u] - mu);
-    }
-    r = inv_root(token_sum<TPT>(s, red) / cnt + p.eps);
+        for (int u = 0; u < 4; ++u) {
+          const float2 d = fsub2(x[i][u], m2);
+          s = ffma2v(d, d, s);
+        }
+    r = inv_root(token_sum<TPT>(s.x + s.y, red) * inv + p.eps);
+    shift = -mu * r;
   }
 
-  float wv[8], bv[8];
-  const bool has_w = t.w != nullptr, has_b = t.b != nullptr;
-  if (!p.all_heads) {
-    if (has_w) nr_weights(t.w, p.w_f32, l, wv);
-    if (has_b) nr_weights(t.b, p.w_f32, l, bv);
-  }
+  // the first chunk's output row; a chunk is TPT / L heads further
+  const int h0 = lane / L;
   const int Hl = p.ranks > 0 ? p.H / p.ranks : p.H;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = i * TPT + lane;
-    float x[8];
-    nr_unpack(raw[i], x);
-    if (p.norm != SAGE_NORM_NONE && !p.all_heads) {
-      mu = 0.f;
+    if (!ALL && p.norm != SAGE_NORM_NONE) {
+      float mu = 0.f;
       if (p.norm == SAGE_NORM_LAYER) {
-        float s = 0.f;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) s += x[u];
-        mu = head_sum<L>(s) / (float)D;
+        float2 s = fadd2(fadd2(x[i][0], x[i][1]), fadd2(x[i][2], x[i][3]));
+        mu = head_sum<L>(s.x + s.y) * (1.f / (float)D);
       }
-      float s = 0.f;
+      const float2 m2 = make_float2(mu, mu);
+      float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) s += (x[u] - mu) * (x[u] - mu);
-      r = inv_root(head_sum<L>(s) / (float)D + p.eps);
+      for (int u = 0; u < 4; ++u) {
+        const float2 d = fsub2(x[i][u], m2);
+        s = ffma2v(d, d, s);
+      }
+      r = inv_root(head_sum<L>(s.x + s.y) * (1.f / (float)D) + p.eps);
+      shift = -mu * r;
     }
     if (p.norm != SAGE_NORM_NONE) {
-      if (p.all_heads && c < nvec) {
-        if (has_w) nr_weights(t.w, p.w_f32, c, wv);
-        if (has_b) nr_weights(t.b, p.w_f32, c, bv);
+      if (ALL && c < nvec) {
+        if (t.w) nr_weights(t.w, p.w_f32, c, wv);
+        if (t.b) nr_weights(t.b, p.w_f32, c, bv);
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        x[u] = (x[u] - mu) * r;
-        if (has_w) x[u] *= wv[u];
-        if (has_b) x[u] += bv[u];
-      }
+      for (int u = 0; u < 4; ++u) x[i][u] = ffma2(x[i][u].x, x[i][u].y, r, shift);
+      if (t.w)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[i][u] = fmul2v(x[i][u], wv[u]);
+      if (t.b)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[i][u] = fadd2(x[i][u], bv[u]);
     }
-    if (p.rope == SAGE_ROPE_INTERLEAVED) {
+    if constexpr (HALF) {
+      // the partner channel c +- d/2 sits L/2 lanes away; every lane of the warp takes part
+      const float sign = l < L / 2 ? -1.f : 1.f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float ox = __shfl_xor_sync(0xffffffffu, x[i][u].x, L / 2), oy = __shfl_xor_sync(0xffffffffu, x[i][u].y, L / 2);
+        if (turn)
+          x[i][u] = make_float2(x[i][u].x * cs[2 * u] + sign * ox * sn[2 * u],
+                                x[i][u].y * cs[2 * u + 1] + sign * oy * sn[2 * u + 1]);
+      }
+    } else {
       if (turn)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float a0 = x[2 * u], a1 = x[2 * u + 1];
-          x[2 * u] = a0 * cs[u] - a1 * sn[u];
-          x[2 * u + 1] = a0 * sn[u] + a1 * cs[u];
-        }
-    } else if (p.rope == SAGE_ROPE_HALF) {
-      // the partner channel c +- d/2 sits L/2 lanes away; every lane of the warp takes part
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const float o = __shfl_xor_sync(0xffffffffu, x[u], L / 2);
-        if (turn) x[u] = l < L / 2 ? x[u] * cs[u] - o * sn[u] : o * sn[u] + x[u] * cs[u];
-      }
+        for (int u = 0; u < 4; ++u)
+          x[i][u] = make_float2(x[i][u].x * cs[u] - x[i][u].y * sn[u], x[i][u].x * sn[u] + x[i][u].y * cs[u]);
     }
     if (c < nvec) {
-      const int h = c / L;
+      const int h = h0 + i * (TPT / L);
       long long out;                       // row of d channels
       if (p.ranks == 0) {
         out = ((long long)b * p.H + h) * p.N + n;
       } else {
-        const int rk = h / Hl;
+        const int rk = (int)((uint32_t)h * p.rank_mul >> 16);
         out = (((long long)rk * p.B + b) * p.N + n) * Hl + (h - rk * Hl);
       }
-      if (SAGE_DCHECK(out * L + l, p.tokens * nvec, kSiteNormOut))
-        t.y[out * L + l] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                      pack_bf16x2(x[6], x[7]));
+      if (SAGE_DCHECK(out * L + l, tokens * nvec, kSiteNormOut))
+        t.y[out * L + l] = make_uint4(pack_bf16x2(x[i][0].x, x[i][0].y), pack_bf16x2(x[i][1].x, x[i][1].y),
+                                      pack_bf16x2(x[i][2].x, x[i][2].y), pack_bf16x2(x[i][3].x, x[i][3].y));
     }
   }
 }
 
 template <int D, int TPT, int CH>
-cudaError_t nr_launch(const NrParams& p, int first, int tensors, cudaStream_t stream) {
-  const long long per = kNrThreads / TPT;
-  const dim3 grid((unsigned)((p.tokens + per - 1) / per), (unsigned)tensors);
-  qk_norm_rope_kernel<D, TPT, CH><<<grid, kNrThreads, 0, stream>>>(p, first);
+cudaError_t nr_launch(const NrParams& p, bool all, bool half, int first, int tensors, cudaStream_t stream) {
+  constexpr int TOKENS = kNrThreads / TPT;
+  const dim3 grid((unsigned)((p.N + TOKENS - 1) / TOKENS), (unsigned)tensors, (unsigned)p.B);
+  if (all && half)
+    qk_norm_rope_kernel<D, TPT, CH, true, true><<<grid, kNrThreads, 0, stream>>>(p, first);
+  else if (all)
+    qk_norm_rope_kernel<D, TPT, CH, true, false><<<grid, kNrThreads, 0, stream>>>(p, first);
+  else if (half)
+    qk_norm_rope_kernel<D, TPT, CH, false, true><<<grid, kNrThreads, 0, stream>>>(p, first);
+  else
+    qk_norm_rope_kernel<D, TPT, CH, false, false><<<grid, kNrThreads, 0, stream>>>(p, first);
   return cudaGetLastError();
 }
 
-// Threads per token by the width: up to 2048 channels one warp holds the row
-// (no block-wide sum), above that a block of four warps.
+// Threads per token by the width: up to 512 channels a warp (no block-wide sum), above
+// that a block of four (a warp with eight chunks a thread took 146 us where the block
+// with two takes 128: 2 x 17776 x 30 x 64, LAYER).
 template <int D>
-cudaError_t nr_dispatch(const NrParams& p, int first, int tensors, cudaStream_t stream) {
+cudaError_t nr_dispatch(const NrParams& p, bool all, bool half, int first, int tensors, cudaStream_t stream) {
   const int nvec = p.H * (D / 8);
-  if (nvec <= 2 * 32) return nr_launch<D, 32, 2>(p, first, tensors, stream);
-  if (nvec <= 8 * 32) return nr_launch<D, 32, 8>(p, first, tensors, stream);
-  if (nvec <= 5 * 128) return nr_launch<D, 128, 5>(p, first, tensors, stream);
-  if (nvec <= 8 * 128) return nr_launch<D, 128, 8>(p, first, tensors, stream);
-  return nr_launch<D, 128, 16>(p, first, tensors, stream);
+  if (nvec <= 2 * 32) return nr_launch<D, 32, 2>(p, all, half, first, tensors, stream);
+  if (nvec <= 2 * 128) return nr_launch<D, 128, 2>(p, all, half, first, tensors, stream);
+  if (nvec <= 5 * 128) return nr_launch<D, 128, 5>(p, all, half, first, tensors, stream);
+  if (nvec <= 8 * 128) return nr_launch<D, 128, 8>(p, all, half, first, tensors, stream);
+  return nr_launch<D, 128, 16>(p, all, half, first, tensors, stream);
 }
 
 }  // namespace
@@ -271,20 +288,21 @@ cudaError_t launch_qk_norm_rope(const void* q, const void* k, long long q_stride
   p.t[1] = NrTensor{static_cast<const uint4*>(k), k_stride / 8, static_cast<uint4*>(k_out), wk, bk};
   p.cos4 = reinterpret_cast<const float4*>(cos_t);
   p.sin4 = reinterpret_cast<const float4*>(sin_t);
-  p.tokens = (long long)B * N;
-  p.N = N;
   p.B = B;
+  p.N = N;
   p.H = H;
   p.norm = norm;
-  p.all_heads = all_heads;
   p.w_f32 = w_f32;
-  p.rope = rope;
   p.begin = rope_begin;
-  p.len = rope_len;
+  p.len = rope == SAGE_ROPE_NONE ? 0 : rope_len;
   p.ranks = ranks;
+  const int Hl = ranks > 0 ? H / ranks : H;
+  p.rank_mul = (65536u + Hl - 1) / Hl;
   p.eps = eps;
+  const bool half = rope == SAGE_ROPE_HALF;
   const int first = q ? 0 : 1, tensors = (q ? 1 : 0) + (k ? 1 : 0);
-  return d == 128 ? nr_dispatch<128>(p, first, tensors, stream) : nr_dispatch<64>(p, first, tensors, stream);
+  return d == 128 ? nr_dispatch<128>(p, all_heads, half, first, tensors, stream)
+                  : nr_dispatch<64>(p, all_heads, half, first, tensors, stream);
 }
 
 }  // namespace sage

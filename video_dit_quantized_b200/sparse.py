@@ -11,7 +11,6 @@ itself are kept from reuse until the work on `stream` is done.
 """
 from __future__ import annotations
 
-import ctypes
 import os
 import re
 
@@ -28,48 +27,51 @@ SELECT_MAX_BLOCKS = 6016
 HEADER = os.path.join(os.path.dirname(sage.HEADER), "sage_sparse.h")
 
 
-class _Call:
-    """The device and stream of one call: checks that every tensor lives on one CUDA device, makes it current
-    for the call and gives device pointers."""
+def _where(stream, names: str, *tensors):
+    """Index of the one CUDA device all given tensors (None: left out) and the stream belong to."""
+    dev = -1
+    for k, t in enumerate(tensors):
+        if t is None:
+            continue
+        d = t.get_device()
+        if d < 0:
+            raise ValueError(f"{names.split()[k]}: a tensor passed for device memory is not a CUDA tensor")
+        if dev < 0:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"{names.split()[k]} is on cuda:{d}, the other tensors on cuda:{dev}")
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{dev}")
+    return dev
 
-    def __init__(self, stream, tensors):
-        import torch
-        self.dev = None
-        for name, t in tensors:
-            if t is None:
-                continue
-            if not t.is_cuda:
-                raise ValueError(f"{name}: a tensor passed for device memory is not a CUDA tensor")
-            if self.dev is None:
-                self.dev = t.device
-            elif t.device != self.dev:
-                raise ValueError(f"{name} is on {t.device}, the other tensors on {self.dev}")
-        if stream is not None and stream.device != self.dev:
-            raise ValueError(f"the stream belongs to {stream.device}, the tensors to {self.dev}")
-        self._guard = torch.cuda.device(self.dev) if torch.cuda.current_device() != self.dev.index else None
-        self._given = stream
-        self.stream = stream if stream is not None else torch.cuda.current_stream(self.dev)
 
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return self
+def _handle(stream, dev: int) -> int:
+    """The stream to launch on: the given one, or the device's current one."""
+    import torch
+    return (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
 
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
 
-    def new(self, shape, dtype, zero=False):
-        """Device memory made for this call: zeroed on the call's stream, not reused before its work is done."""
-        import torch
-        if self._given is None:
-            return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=self.dev)
-        with torch.cuda.stream(self.stream):
-            return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=self.dev)
+def _launch(what: str, dev: int, *args):
+    """Calls a C entry point with the tensors' device current."""
+    import torch
+    f = getattr(sage.LIB, what)
+    if torch.cuda.current_device() == dev:
+        rc = f(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args)
+    _check(rc, what)
 
-    @property
-    def handle(self):
-        return self.stream.cuda_stream
+
+def _new(shape, dtype, dev: int, stream, zero: bool = False):
+    """Device memory made for one call, of the stream that the call runs on: zeroed there, and not given to
+    anyone else before that stream is done with it."""
+    import torch
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=f"cuda:{dev}")
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=f"cuda:{dev}")
 
 
 def _p(t):
@@ -145,17 +147,15 @@ def qk_norm_rope(q, k=None, wq=None, wk=None, bq=None, bk=None, norm: int = NORM
         if src is None and t is not None:
             raise ValueError(f"{name} has no input")
         _need(t, name, torch.bfloat16, out_shape, optional=True)
-    with _Call(stream, (("q", q), ("k", k), ("wq", wq), ("wk", wk), ("bq", bq), ("bk", bk), ("cos", cos), ("sin", sin),
-                        ("q_out", q_out), ("k_out", k_out))) as call:
-        if q is not None and q_out is None:
-            q_out = call.new(out_shape, torch.bfloat16)
-        if k is not None and k_out is None:
-            k_out = call.new(out_shape, torch.bfloat16)
-        _check(sage.LIB.sage_qk_norm_rope(_p(q), _p(k), q_row, k_row, _p(wq), _p(bq), _p(wk), _p(bk),
-                                          sage.DTYPE_F32 if w_dtype == torch.float32 else sage.DTYPE_BF16, _p(cos),
-                                          _p(sin), B, N, H, d, int(norm), int(scope), float(eps), int(rope),
-                                          int(rope_begin), rope_len, _p(q_out), _p(k_out), int(ranks), call.handle),
-               "sage_qk_norm_rope")
+    dev = _where(stream, "q k wq wk bq bk cos sin q_out k_out", q, k, wq, wk, bq, bk, cos, sin, q_out, k_out)
+    if q is not None and q_out is None:
+        q_out = _new(out_shape, torch.bfloat16, dev, stream)
+    if k is not None and k_out is None:
+        k_out = _new(out_shape, torch.bfloat16, dev, stream)
+    _launch("sage_qk_norm_rope", dev, _p(q), _p(k), q_row, k_row, _p(wq), _p(bq), _p(wk), _p(bk),
+            sage.DTYPE_F32 if w_dtype == torch.float32 else sage.DTYPE_BF16, _p(cos), _p(sin), B, N, H, d, int(norm),
+            int(scope), float(eps), int(rope), int(rope_begin), rope_len, _p(q_out), _p(k_out), int(ranks),
+            _handle(stream, dev))
     return q_out, k_out
 
 
@@ -186,16 +186,15 @@ def select_blocks(q, k, keep: int, first: int = 0, window: int = 0, lists=None, 
     _need(lists, "lists", torch.int32, (B, H, nT, keep), optional=True)
     _need(counts, "counts", torch.int32, (B, H, nT), optional=True)
     _need(scratch, "scratch", torch.uint8, optional=True)
-    with _Call(stream, (("q", q), ("k", k), ("lists", lists), ("counts", counts), ("scratch", scratch))) as call:
-        if scratch is None:
-            n = select_scratch_bytes(B, H, N, d)
-            scratch = call.new(max(n, 16), torch.uint8)
-        if lists is None:
-            lists = call.new((B, H, nT, keep), torch.int32)
-        if counts is None:
-            counts = call.new((B, H, nT), torch.int32)
-        _check(sage.LIB.sage_select_blocks(_p(q), _p(k), B, H, N, d, int(keep), int(first), int(window), _p(lists),
-                                           _p(counts), _p(scratch), scratch.numel(), call.handle), "sage_select_blocks")
+    dev = _where(stream, "q k lists counts scratch", q, k, lists, counts, scratch)
+    if scratch is None:
+        scratch = _new(max(select_scratch_bytes(B, H, N, d), 16), torch.uint8, dev, stream)
+    if lists is None:
+        lists = _new((B, H, nT, keep), torch.int32, dev, stream)
+    if counts is None:
+        counts = _new((B, H, nT), torch.int32, dev, stream)
+    _launch("sage_select_blocks", dev, _p(q), _p(k), B, H, N, d, int(keep), int(first), int(window), _p(lists),
+            _p(counts), _p(scratch), scratch.numel(), _handle(stream, dev))
     return lists, counts
 
 
@@ -224,31 +223,25 @@ def attn_fwd_sparse(q, k, v, mode: int, lists, counts, coeff: int = COEFF_DIVIDE
     """
     import torch
     B, H, N, d = _sparse_args(q, k, v, o, lists, counts, workspace)
-    with _Call(stream, (("q", q), ("k", k), ("v", v), ("o", o), ("lists", lists), ("counts", counts),
-                        ("workspace", workspace))) as call:
-        if o is None:
-            o = call.new((B, H, N, d), torch.bfloat16)
-        if workspace is None:
-            n = sage.workspace_bytes(B, H, N, d, mode)
-            if n == 0:
-                raise SageError(EINVAL, "sage_workspace_bytes")
-            workspace = call.new(n, torch.uint8, zero=True)
-        _check(sage.LIB.sage_attn_fwd_sparse(_p(q), _p(k), _p(v), _p(o), B, H, N, d, int(mode), _p(lists), _p(counts),
-                                             lists.shape[3], int(coeff), _p(workspace),
-                                             workspace.numel() * workspace.element_size(), call.handle),
-               "sage_attn_fwd_sparse")
+    dev = _where(stream, "q k v o lists counts workspace", q, k, v, o, lists, counts, workspace)
+    if o is None:
+        o = _new((B, H, N, d), torch.bfloat16, dev, stream)
+    if workspace is None:
+        n = sage.workspace_bytes(B, H, N, d, mode)
+        if n == 0:
+            raise SageError(EINVAL, "sage_workspace_bytes")
+        workspace = _new(n, torch.uint8, dev, stream, zero=True)
+    _launch("sage_attn_fwd_sparse", dev, _p(q), _p(k), _p(v), _p(o), B, H, N, d, int(mode), _p(lists),
+            _p(counts), lists.shape[3], int(coeff), _p(workspace), workspace.numel() * workspace.element_size(), _handle(stream, dev))
     return o
 
 
 def dbg_sparse_forced_timeout(q, k, v, mode: int, lists, counts, workspace, timeout_cycles: int, stream=None):
     import torch
     B, H, N, d = _sparse_args(q, k, v, None, lists, counts, workspace)
-    with _Call(stream, (("q", q), ("k", k), ("v", v), ("lists", lists), ("counts", counts),
-                        ("workspace", workspace))) as call:
-        o = call.new((B, H, N, d), torch.bfloat16)
-        _check(sage.LIB.sage_dbg_sparse_forced_timeout(_p(q), _p(k), _p(v), _p(o), B, H, N, d, int(mode), _p(lists),
-                                                       _p(counts), lists.shape[3], COEFF_DIVIDE, _p(workspace),
-                                                       workspace.numel() * workspace.element_size(),
-                                                       int(timeout_cycles), call.handle),
-               "sage_dbg_sparse_forced_timeout")
+    dev = _where(stream, "q k v lists counts workspace", q, k, v, lists, counts, workspace)
+    o = _new((B, H, N, d), torch.bfloat16, dev, stream)
+    _launch("sage_dbg_sparse_forced_timeout", dev, _p(q), _p(k), _p(v), _p(o), B, H, N, d, int(mode),
+            _p(lists), _p(counts), lists.shape[3], COEFF_DIVIDE, _p(workspace), workspace.numel() * workspace.element_size(),
+            int(timeout_cycles), _handle(stream, dev))
     return o
