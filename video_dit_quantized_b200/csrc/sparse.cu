@@ -56,6 +56,7 @@ struct SparseParams {
   long long timeout;
   int dbg_flags;          // bit 0: the MMA threads first wait on a barrier nobody arrives on
   int q_per_token;
+  int wide;               // o is 32-byte aligned: 32-byte stores
 };
 
 // One item as its consumers see it.  steps -1: no more items.
@@ -77,7 +78,7 @@ struct SparseCfg {
   static constexpr int OFF_V = OFF_K + 2 * KS * TILE_BYTES;       // [2][VS]
   static constexpr int OFF_P = OFF_V + 2 * VS * TILE_BYTES;       // [2], QUANT
   static constexpr int OFF_LANE = OFF_P + 2 * C::P_BYTES;
-  static constexpr int LANE_BYTES = 256;
+  static constexpr int LANE_BYTES = 1280;
   static constexpr int SMEM_BYTES = OFF_LANE + 2 * LANE_BYTES + 64 + 1024;   // + 1 KB alignment slack
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
@@ -85,6 +86,7 @@ struct SparseCfg {
 // What the threads of one lane share.
 template <int KS, int VS>
 struct Lane {
+  float v_scale[2][128];            // QUANT: of the items' heads, alternating
   Item item[2];
   uint64_t q_full, q_empty;
   uint64_t k_full[KS], k_empty[KS];
@@ -96,6 +98,14 @@ struct Lane {
   uint64_t tok;                     // this lane's turn on the exponential phase
   uint64_t item_full[2], item_empty[2];
 };
+
+// 32 bytes (32-byte aligned): rows lie 2 D bytes apart, so a warp's store touches 32
+// lines whatever its width, and wider stores mean fewer of them.
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 
 template <int D, bool QUANT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -331,29 +341,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     // so l accumulates 448 * sum(p) and the epilogue divides by it directly.
     constexpr float kLog2PScale = QUANT ? 8.807354922057604f : 0.f;
 
-    for (int n = 0; ok; ++n) {
-      if (!mbar_wait(&b.item_full[n & 1], (n >> 1) & 1, abort_flag, limit)) { ok = false; break; }
+    // The item at hand and what its first step needs, read while the previous item is stored.
+    Item it{0, 0, -1, 0};
+    int blk_next = 0, blk_after = 0;                     // the next two blocks of its list
+    float qs = 0.f, ks_next = 0.f, vsc = 0.f;            // QUANT: this row's Q scale, the next block's K scale, a V scale
+    auto listed = [&](int j) {
+      const long long at = ((long long)it.bh * nT + it.qb) * prm.width + j;
+      return j < it.steps && SAGE_DCHECK(at, (long long)prm.items * prm.width, kSiteSparseList) ? __ldg(prm.lists + at) : 0;
+    };
+    auto scale_of = [&](int x) {
+      const long long ki = (long long)it.bh * nT + ((unsigned)x < (unsigned)nT ? x : 0);
+      return QUANT && SAGE_DCHECK(ki, (long long)prm.items, kSiteSparseScale) ? __ldg(prm.k_scale + ki) : 0.f;
+    };
+    auto take_item = [&](int n) {
+      if (!mbar_wait(&b.item_full[n & 1], (n >> 1) & 1, abort_flag, limit)) return false;
       const volatile Item* vi = &b.item[n & 1];
-      Item it{vi->bh, vi->qb, vi->steps, vi->bad};
+      it = Item{vi->bh, vi->qb, vi->steps, vi->bad};
       mbar_arrive(&b.item_empty[n & 1]);
-      const int c = it.steps;
-      float qs = 0.f;
-      if (QUANT && c > 0) {
+      blk_next = listed(0);
+      blk_after = listed(1);
+      if (QUANT && it.steps > 0) {
         const size_t qi = prm.q_per_token ? (size_t)it.bh * prm.Npad + it.qb * 128 + row : (size_t)it.bh * nT + it.qb;
         if (SAGE_DCHECK(qi, (long long)prm.BH * (prm.q_per_token ? prm.Npad : nT), kSiteSparseScale)) qs = __ldg(prm.q_scale + qi);
+        if (row < D && SAGE_DCHECK((size_t)it.bh * D + row, (long long)prm.BH * D, kSiteSparseScale))
+          vsc = __ldg(prm.v_scale + (size_t)it.bh * D + row);
       }
+      return true;
+    };
+    ok = take_item(0);
+    ks_next = scale_of(blk_next);
+    for (int n = 0; ok; ++n) {
+      const int c = it.steps;
+      if (c < 0) break;
+      // every thread's value reaches the others through p_full, the MMA thread and o_ready
+      if (QUANT && c > 0 && row < D) b.v_scale[n & 1][row] = vsc;
       float m = -INFINITY, l = 0.f;
-      const long long off = ((long long)it.bh * nT + it.qb) * prm.width;
-      auto listed = [&](int j) {
-        return j < c && SAGE_DCHECK(off + j, (long long)prm.items * prm.width, kSiteSparseList) ? __ldg(prm.lists + off + j) : 0;
-      };
-      auto scale_of = [&](int x) {
-        const long long ki = (long long)it.bh * nT + ((unsigned)x < (unsigned)nT ? x : 0);
-        return QUANT && SAGE_DCHECK(ki, (long long)prm.items, kSiteSparseScale) ? __ldg(prm.k_scale + ki) : 0.f;
-      };
-      // the next step's block (and its scale) and the block after it are read ahead
-      int blk_next = listed(0), blk_after = listed(1);
-      float ks_next = scale_of(blk_next);
       for (int j = 0; j < c; ++j) {
         const int blk = blk_next;
         const float sc = QUANT ? __fmul_rn(__fmul_rn(qs, ks_next), softmax_c(D)) : softmax_c(D);
@@ -485,22 +507,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++step;
       }
       if (!ok) break;
-      if (c < 0) break;
       if (it.bad && row == 0) atomicOr(prm.status, kStatusBadIndex);
+      const int gq = it.qb * 128 + row;
+      const long long orow = ((long long)it.bh * N + gq) * D;
+      if (!(ok = take_item(n + 1))) break;
       if (c > 0) {
         if (!mbar_wait(&b.o_ready, (QUANT ? step - 1 : done) & 1, abort_flag, limit)) { ok = false; break; }
         ++done;
         tc_fence_after();
       }
-      const int gq = it.qb * 128 + row;
-      const long long orow = ((long long)it.bh * N + gq) * D;
-      const float* vs = prm.v_scale + (size_t)it.bh * D;
-      const bool vs_ok = !QUANT || SAGE_DCHECK((size_t)it.bh * D + D - 1, (long long)prm.BH * D, kSiteSparseScale);
+      ks_next = scale_of(blk_next);
+      // ---------------------------------------------------------- epilogue
       // bf16(a / l) for 32 columns at a time without 32 divisions: 1 / l lies between
       // the two neighbours of its rounded value, so a / l rounds between the products
       // with them; where both give the same bf16 that is the result, else divide.
       const float rl = __frcp_rn(l);
       const float rlo = __uint_as_float(__float_as_uint(rl) - 1u), rhi = __uint_as_float(__float_as_uint(rl) + 1u);
+      const float4* vs4 = reinterpret_cast<const float4*>(b.v_scale[n & 1]);
 #pragma unroll
       for (int ch = 0; ch < D / 32; ++ch) {
         uint32_t w[16];
@@ -514,11 +537,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (QUANT) {
 #pragma unroll
             for (int g = 0; g < 8; ++g) {
-              const float4 v4 = vs_ok ? __ldg(reinterpret_cast<const float4*>(vs + ch * 32) + g) : make_float4(0.f, 0.f, 0.f, 0.f);
-              a[2 * g].x = __fmul_rn(a[2 * g].x, v4.x);
-              a[2 * g].y = __fmul_rn(a[2 * g].y, v4.y);
-              a[2 * g + 1].x = __fmul_rn(a[2 * g + 1].x, v4.z);
-              a[2 * g + 1].y = __fmul_rn(a[2 * g + 1].y, v4.w);
+              const float4 v4 = vs4[ch * 8 + g];
+              a[2 * g] = fmul2v(a[2 * g], make_float2(v4.x, v4.y));
+              a[2 * g + 1] = fmul2v(a[2 * g + 1], make_float2(v4.z, v4.w));
             }
           }
           uint32_t apart = 0;
@@ -535,12 +556,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c == 0 || l == 0.f)                  // no block, or none inside the sequence
 #pragma unroll
           for (int g = 0; g < 16; ++g) w[g] = 0u;
-        if (gq < N) {
-          uint4* dst = reinterpret_cast<uint4*>(prm.o + orow + ch * 32);
+        if (gq < N && SAGE_DCHECK((orow + ch * 32) / 8 + 3, (long long)prm.BH * N * D / 8, kSiteSparseOut)) {
+          __nv_bfloat16* dst = prm.o + orow + ch * 32;
+          if (prm.wide) {
+            store32(dst, w);
+            store32(dst + 16, w + 8);
+          } else {
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            if (SAGE_DCHECK((orow + ch * 32) / 8 + v, (long long)prm.BH * N * D / 8, kSiteSparseOut))
-              dst[v] = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+            for (int v = 0; v < 4; ++v)
+              reinterpret_cast<uint4*>(dst)[v] = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+          }
         }
       }
     }
@@ -616,7 +641,7 @@ cudaError_t launch_sparse_i8f8(const int8_t* q_i8, const float* q_scale, const i
     return cudaErrorInvalidValue;
   const SparseParams prm{q_scale, k_scale, v_scale, static_cast<__nv_bfloat16*>(o), lists, counts, status,
                          status + kNextWord, N, nT, Npad, width, BH, BH * nT, timeout_cycles, dbg_flags,
-                         q_per_token ? 1 : 0};
+                         q_per_token ? 1 : 0, (reinterpret_cast<uintptr_t>(o) & 31u) == 0};
   return d == 128 ? launch_sparse_d<128, true>(tq, tk, tv, prm, stream)
                   : launch_sparse_d<64, true>(tq, tk, tv, prm, stream);
 }
@@ -635,7 +660,8 @@ cudaError_t launch_sparse_bf16(const void* q, const void* k, const void* v, void
                       CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   const SparseParams prm{nullptr, nullptr, nullptr, static_cast<__nv_bfloat16*>(o), lists, counts, status,
-                         status + kNextWord, N, nT, nT * kTile, width, BH, BH * nT, timeout_cycles, dbg_flags, 0};
+                         status + kNextWord, N, nT, nT * kTile, width, BH, BH * nT, timeout_cycles, dbg_flags, 0,
+                         (reinterpret_cast<uintptr_t>(o) & 31u) == 0};
   return d == 128 ? launch_sparse_d<128, false>(tq, tk, tv, prm, stream)
                   : launch_sparse_d<64, false>(tq, tk, tv, prm, stream);
 }
