@@ -84,7 +84,8 @@ def test_select_refusals():
     f = sage.LIB.sage_select_blocks
     a, odd = VP(1 << 30), VP((1 << 30) + 8)
     n = sparse.select_scratch_bytes(1, 2, 1000, 128)
-    assert n == -(-2 * 2 * 8 * 129 * 4 // 256) * 256
+    rows = 2 * 2 * 8                     # means, three slices, a step and a norm for every block of q and k
+    assert n == rows * 128 * 4 + rows * 3 * 128 + 2 * 256
     ok = lambda q=a, k=a, B=1, H=2, N=1000, d=128, keep=3, first=0, window=0, li=a, co=a, sc=a, nb=n: f(
         q, k, B, H, N, d, keep, first, window, li, co, sc, nb, None)
     for kw in (dict(q=None), dict(k=odd), dict(B=0), dict(N=0), dict(keep=0), dict(first=-1), dict(window=-2),
