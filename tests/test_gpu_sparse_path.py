@@ -200,3 +200,41 @@ def test_full_lists_have_no_error_against_the_dense_layer(cuda_dev):
         errs.append(float(sage.rel_l2(o, dense)))
     assert errs[-1] == 0.0
     assert all(a > b for a, b in zip(errs, errs[1:])), errs
+
+
+@pytest.mark.parametrize("P,mode", [(1, I8), (2, I8), (4, BF16)])
+def test_ulysses_send_of_normed_queries_and_keys(P, mode, cuda_dev):
+    """send_qk over P emulated ranks (each with its tokens' tables) is norm, rotation and attention of the whole
+    sequence, bit for bit."""
+    from video_dit_quantized_b200 import sage, sparse
+    from video_dit_quantized_b200.ulysses import UlyssesAttention
+    B, N, H, d = 2, 640, 8, 128
+    Nl = N // P
+    qkv, w, cos, sin = projections(B, N, H, d, 41, cuda_dev)
+    norm = dict(wq=w[0], wk=w[1], norm=sparse.NORM_RMS, scope=sparse.NORM_SCOPE_ALL)
+    q, k = sparse.qk_norm_rope(qkv[:, :, 0], qkv[:, :, 1], cos=cos, sin=sin, **norm)
+    v = qkv[:, :, 2].permute(0, 2, 1, 3).contiguous()
+    ref = sage.attn_fwd(q, k, v, mode).permute(0, 2, 1, 3)
+    sent = [[] for _ in range(P)]
+    ranks = [UlyssesAttention(B, Nl, H, d, P, mode=mode, device=cuda_dev,
+                              a2a=lambda out, inp, r=r: sent[r].append((out, inp))) for r in range(P)]
+
+    def exchange():
+        for slot in range(len(sent[0])):
+            for r in range(P):
+                for src in range(P):
+                    sent[r][slot][0][src].copy_(sent[src][slot][1][r])
+        for s in sent:
+            s.clear()
+
+    for again in range(2):
+        for r, ua in enumerate(ranks):
+            part = qkv[:, r * Nl:(r + 1) * Nl].contiguous()
+            ua.send_qk(part[:, :, 0], part[:, :, 1], cos=cos[r * Nl:(r + 1) * Nl], sin=sin[r * Nl:(r + 1) * Nl], **norm)
+            ua.send("v", part[:, :, 2])
+        exchange()
+        for ua in ranks:
+            ua.attend_local()
+        exchange()
+        got = torch.cat([ua.finish().clone() for ua in ranks], dim=1)
+        assert torch.equal(bits(got), bits(ref.contiguous())), again

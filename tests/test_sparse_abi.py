@@ -155,3 +155,38 @@ def test_binding_refuses_what_the_c_abi_cannot_see():
         sparse.attn_fwd_sparse(q, q, q, 0, li, co[:, :1].contiguous())
     with pytest.raises(ValueError, match="not a CUDA tensor"):
         sparse.attn_fwd_sparse(q, q, q, 0, li, co)
+
+
+def test_ulysses_send_qk_on_the_host():
+    """send_qk fills the send layout through norm_rope, starts both exchanges and refuses other shapes (CPU, with a
+    stand-in for the kernel: the layout of the send copy)."""
+    import sys
+    sys.path.insert(0, "tests")
+    from _util import attention_seqpar_ref, ulysses_ref_permute
+    from video_dit_quantized_b200.ulysses import UlyssesAttention
+    calls, sent = [], []
+
+    def norm_rope(q, k, ranks, q_out, k_out, **kw):
+        calls.append(kw)
+        for x, y in ((q, q_out), (k, k_out)):
+            ulysses_ref_permute(2 * x, y, 1, 8, 4, 16, ranks, 0)
+
+    for P in (1, 2):
+        calls.clear()
+        sent.clear()
+        ua = UlyssesAttention(1, 8, 4, 16, P, mode=sage.MODE_BF16, device="cpu", permute=ulysses_ref_permute,
+                              attention=attention_seqpar_ref, a2a=lambda o, i: sent.append((o, i)), norm_rope=norm_rope)
+        x = torch.randn(1, 8, 4, 16).to(torch.bfloat16)
+        with pytest.raises(ValueError, match="k must be"):
+            ua.send_qk(x, x[:, :4], eps=1e-5)
+        ua.send_qk(x, 3 * x, eps=1e-5)
+        assert calls == [dict(eps=1e-5)]
+        want = torch.empty(P, 1, 8, 4 // P, 16, dtype=torch.bfloat16)
+        ulysses_ref_permute(2 * x, want, 1, 8, 4, 16, P, 0)
+        if P == 1:
+            assert sent == [] and torch.equal(ua._keep["q"], want)
+        else:
+            assert [o is ua.recv_buf[t] for (o, _), t in zip(sent, "qk")] == [True, True]
+            assert torch.equal(sent[0][1], want)
+        with pytest.raises(RuntimeError, match="v"):
+            ua.attend_local()

@@ -46,7 +46,11 @@ namespace sage {
 
 namespace {
 
-constexpr int kPoolThreads = 256;
+// One thread a channel: few threads with many loads each keep more bytes in flight per
+// thread slot than the long tail of sums costs (280 us with 256 threads at 1 x 40 x 75600
+// x 128, 262 with 128; 1 x 30 x 17776 x 64: 37 with 256, 28 with 64).
+template <int D>
+constexpr int kPoolThreads = D;
 
 // What the pool kernel leaves in the scratch: the rounded means [2][BH][nT][D] (q, then
 // k), their slices [2][3][BH][nT][D], steps and norms (a little rounded up) [2][BH][nT].
@@ -59,10 +63,10 @@ struct Pooled {
 
 // grid (nT, BH, 2): z = 0 pools q, z = 1 pools k
 template <int D>
-__global__ void __launch_bounds__(kPoolThreads) pool_blocks_kernel(const uint4* __restrict__ q,
+__global__ void __launch_bounds__(kPoolThreads<D>) pool_blocks_kernel(const uint4* __restrict__ q,
                                                                    const uint4* __restrict__ k, int N, int nT,
                                                                    const Pooled out) {
-  constexpr int V8 = D / 8, GROUPS = kPoolThreads / V8, PER_T = kTile / GROUPS;
+  constexpr int V8 = D / 8, GROUPS = kPoolThreads<D> / V8, PER_T = kTile / GROUPS;
   __shared__ double part[GROUPS][D + 2];
   __shared__ float norm_part[D / 32], amax_part[D / 32];
   const int blk = blockIdx.x, bh = blockIdx.y;
@@ -656,7 +660,7 @@ cudaError_t select_d(const void* q, const void* k, int BH, int N, int keep, int 
                      int* counts, void* scratch, cudaStream_t stream) {
   const int nT = num_tiles(N);
   const Pooled pooled = pooled_carve(scratch, BH, nT, D);
-  pool_blocks_kernel<D><<<dim3(nT, BH, 2), kPoolThreads, 0, stream>>>(static_cast<const uint4*>(q),
+  pool_blocks_kernel<D><<<dim3(nT, BH, 2), kPoolThreads<D>, 0, stream>>>(static_cast<const uint4*>(q),
                                                                       static_cast<const uint4*>(k), N, nT, pooled);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;

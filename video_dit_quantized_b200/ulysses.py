@@ -9,7 +9,8 @@ the output to the sequence slices.  The all-to-all of q, k and v cost about
 each exchange as soon as its tensor is computed, while the next projection
 still runs.  `UlyssesAttention.send` does exactly that: each of q, k, v goes
 into its send layout and its all-to-all starts at once (asynchronously, on
-the communicator's stream); `attend` waits for the three, runs the attention
+the communicator's stream); `send_qk` writes the send layout of q and k from
+their norm and rotation, without the copy; `attend` waits for the three, runs the attention
 path on the local heads and brings O back.
 
 Per rank: inputs [B, Nl, H, d] (this rank's Nl = N / P tokens, all heads),
@@ -27,7 +28,7 @@ The collectives are torch.distributed's `all_to_all_single` (NCCL on GPUs).
 """
 from __future__ import annotations
 
-from . import sage
+from . import sage, sparse
 
 
 def _default_a2a(group):
@@ -43,11 +44,12 @@ class UlyssesAttention:
 
     permute(src, dst, B, Nl, H, d, P, op) and attention(q, k, v, mode, o, workspace) default to the
     CUDA kernels (`attention` takes and gives the [P][B][Nl][Hl][d] exchange layout); a2a(out, inp)
-    -> handle defaults to an asynchronous all_to_all_single on `group`.
+    -> handle defaults to an asynchronous all_to_all_single on `group`; norm_rope(q, k, ranks=, q_out=, k_out=,
+    **norm) defaults to sparse.qk_norm_rope.
     """
 
     def __init__(self, B: int, Nl: int, H: int, d: int, world: int, mode: int = sage.MODE_INT8_FP8,
-                 device=None, group=None, permute=None, attention=None, a2a=None):
+                 device=None, group=None, permute=None, attention=None, a2a=None, norm_rope=None):
         import torch
         if H % world:
             raise ValueError(f"H={H} is not divisible by the {world} ranks")
@@ -70,6 +72,8 @@ class UlyssesAttention:
         self._attention = attention or (
             lambda q, k, v, m, o, ws: sage.attn_fwd_seqpar(q, k, v, m, o, world, workspace=ws))
         self._a2a = a2a or _default_a2a(group)
+        self._norm_rope = norm_rope or sparse.qk_norm_rope
+        self._normed = {}
         self._pending = {}
         self._keep = {}
 
@@ -92,6 +96,29 @@ class UlyssesAttention:
         src = self.send_buf[which]
         self._permute(x, src, *self._geom(sage.ULYSSES_SEND))
         self._pending[which] = self._a2a(self.recv_buf[which], src)
+
+    def send_qk(self, q, k, **norm):
+        """send() of q and k straight from the projections: their norm and position rotation (the arguments of
+        sparse.qk_norm_rope; the tables are those of this rank's tokens) write the send layout themselves, so no
+        copy runs before the all-to-alls."""
+        import torch
+        shape = (self.B, self.Nl, self.H, self.d)
+        for name, x in (("q", q), ("k", k)):
+            if tuple(x.shape) != shape:
+                raise ValueError(f"{name} must be [B, Nl, H, d] = {shape}")
+        out = self.send_buf
+        if self.P == 1:
+            # the exchange of one rank is the identity: attention reads the normed tensors themselves
+            if not self._normed:
+                self._normed = {t: torch.empty((1,) + shape, dtype=torch.bfloat16, device=self.o_send.device) for t in "qk"}
+            out = self._normed
+        self._norm_rope(q, k, ranks=self.P, q_out=out["q"], k_out=out["k"], **norm)
+        for t in "qk":
+            if self.P == 1:
+                self._keep[t] = out[t]
+                self._pending[t] = None
+            else:
+                self._pending[t] = self._a2a(self.recv_buf[t], out[t])
 
     def attend_local(self):
         """Wait for q, k, v, run attention on the local heads (O lands in the send layout) and start
