@@ -69,6 +69,8 @@ __global__ void __launch_bounds__(kPoolThreads<D>) pool_blocks_kernel(const uint
   constexpr int V8 = D / 8, GROUPS = kPoolThreads<D> / V8, PER_T = kTile / GROUPS;
   __shared__ double part[GROUPS][D + 2];
   __shared__ float norm_part[D / 32], amax_part[D / 32];
+  // the score kernel's blocks may take their places once every block of this grid has started
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int blk = blockIdx.x, bh = blockIdx.y;
   const int n0 = blk * kTile, nr = min(kTile, N - n0);
   const uint4* src = (blockIdx.z == 0 ? q : k);
@@ -497,19 +499,25 @@ __global__ void __launch_bounds__(kScoreThreads, ROWS == kRows ? 2 : 1)
     for (int sl = 0; sl < 3; ++sl)
       tma_load_2d(sm + sl * C::KEY_BYTES, &tmK, &full, 0, ((3 + sl) * (int)gridDim.y + bh) * nT + x * kKeys);
   };
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, 128);                   // two sets of accumulators
+    tmem_relinquish();
+  }
   if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmQ);
     mbar_init(&full, 1);
     mbar_init(&done, 1);
     gave_up = 0;
     fence_mbar_init();
+  }
+  // launched while the pool kernel still runs: nothing of it is read before this
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (threadIdx.x == 0) {
     fetch_keys(0);
 #pragma unroll
     for (int sl = 0; sl < 3; ++sl)
       tma_load_2d(sm + C::OFF_Q + sl * C::ROW_BYTES, &tmQ, &full, 0, (sl * (int)gridDim.y + bh) * nT + i0);
-  }
-  if (warp == 1) {
-    tmem_alloc(&tmem_slot, 128);                   // two sets of accumulators
-    tmem_relinquish();
   }
   if (threadIdx.x < kRows) later[threadIdx.x] = 0;
   float sq[ROWS];
@@ -633,8 +641,18 @@ cudaError_t score_launch(const SelectParams& p, int BH, cudaStream_t stream) {
   const int smem = (int)ScoreCfg<D>::smem(ROWS, p.nTp);
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<dim3((p.nT + ROWS - 1) / ROWS, BH), kScoreThreads, smem, stream>>>(tk, tq, p);
-  return cudaGetLastError();
+  // its blocks may start, and set themselves up, while the pool kernel's last ones run
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((p.nT + ROWS - 1) / ROWS, BH);
+  cfg.blockDim = dim3(kScoreThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tk, tq, p);
 }
 
 constexpr size_t kSmemMax = 232448 - 2048;       // beside the static arrays

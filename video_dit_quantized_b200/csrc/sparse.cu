@@ -551,7 +551,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (apart)
 #pragma unroll
-            for (int g = 0; g < 16; ++g) w[g] = pack_bf16x2(__fdiv_rn(a[g].x, l), __fdiv_rn(a[g].y, l));   // QUANT: l holds 448 * sum(p)
+            for (int g = 0; g < 16; ++g) {
+              const float2 hi = fmul2(a[g], rhi);
+              if (w[g] != pack_bf16x2(hi.x, hi.y))
+                w[g] = pack_bf16x2(__fdiv_rn(a[g].x, l), __fdiv_rn(a[g].y, l));   // QUANT: l holds 448 * sum(p)
+            }
         }
         if (c == 0 || l == 0.f)                  // no block, or none inside the sequence
 #pragma unroll

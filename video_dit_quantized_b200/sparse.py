@@ -14,6 +14,8 @@ from __future__ import annotations
 import os
 import re
 
+import torch
+
 from . import sage
 from .sage import BLK, EINVAL, SageError, _check, _need
 
@@ -29,17 +31,19 @@ HEADER = os.path.join(os.path.dirname(sage.HEADER), "sage_sparse.h")
 
 def _where(stream, names: str, *tensors):
     """Index of the one CUDA device all given tensors (None: left out) and the stream belong to."""
-    dev = -1
-    for k, t in enumerate(tensors):
-        if t is None:
-            continue
-        d = t.get_device()
-        if d < 0:
-            raise ValueError(f"{names.split()[k]}: a tensor passed for device memory is not a CUDA tensor")
-        if dev < 0:
-            dev = d
-        elif d != dev:
-            raise ValueError(f"{names.split()[k]} is on cuda:{d}, the other tensors on cuda:{dev}")
+    where = {t.get_device() for t in tensors if t is not None}
+    dev = where.pop()
+    if dev < 0 or where:
+        dev = -1
+        for name, t in zip(names.split(), tensors):
+            if t is None:
+                continue
+            d = t.get_device()
+            if d < 0:
+                raise ValueError(f"{name}: a tensor passed for device memory is not a CUDA tensor")
+            dev = d if dev < 0 else dev
+            if d != dev:
+                raise ValueError(f"{name} is on cuda:{d}, the other tensors on cuda:{dev}")
     if stream is not None and stream.device.index != dev:
         raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{dev}")
     return dev
@@ -47,15 +51,13 @@ def _where(stream, names: str, *tensors):
 
 def _handle(stream, dev: int) -> int:
     """The stream to launch on: the given one, or the device's current one."""
-    import torch
-    return (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _launch(what: str, dev: int, *args):
     """Calls a C entry point with the tensors' device current."""
-    import torch
     f = getattr(sage.LIB, what)
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         rc = f(*args)
     else:
         with torch.cuda.device(dev):
@@ -66,12 +68,20 @@ def _launch(what: str, dev: int, *args):
 def _new(shape, dtype, dev: int, stream, zero: bool = False):
     """Device memory made for one call, of the stream that the call runs on: zeroed there, and not given to
     anyone else before that stream is done with it."""
-    import torch
     make = torch.zeros if zero else torch.empty
     if stream is None:
         return make(shape, dtype=dtype, device=f"cuda:{dev}")
     with torch.cuda.stream(stream):
         return make(shape, dtype=dtype, device=f"cuda:{dev}")
+
+
+def _is(t, name, dtype, shape, optional=False):
+    """_need, with the checks of a good tensor in one expression."""
+    if t is None:
+        if not optional:
+            _need(t, name, dtype, shape)
+    elif t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _need(t, name, dtype, shape)
 
 
 def _p(t):
@@ -87,12 +97,11 @@ def header_functions() -> list[str]:
 def _rows(t, name, shape):
     """Row stride in elements of a [B, N, H, d] tensor whose H * d channels are contiguous and whose batches
     follow one another."""
-    import torch
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    B, N, H, d = t.shape
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    B, N, H, d = shape
     sb, sn, sh, sd = t.stride()
     # the stride of a dimension of one element says nothing
     row = sn if N > 1 else (sb if B > 1 else H * d)
@@ -112,7 +121,6 @@ def qk_norm_rope(q, k=None, wq=None, wk=None, bq=None, bk=None, norm: int = NORM
     ROPE_NONE; without tables nothing is rotated).  Weights: bf16 or fp32, all of one type, [d] (per head) or
     [H * d] (over all heads).
     """
-    import torch
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k is required")
@@ -125,10 +133,11 @@ def qk_norm_rope(q, k=None, wq=None, wk=None, bq=None, bk=None, norm: int = NORM
         rope, cos, sin, rope_len = ROPE_NONE, None, None, 0
         rope_begin = 0
     else:
-        _need(cos, "cos", torch.float32)
+        if cos is None or cos.dim() != 2:
+            _need(cos, "cos", torch.float32, ("rope_len", d // 2))
         rope_len = cos.shape[0]
-        _need(cos, "cos", torch.float32, (rope_len, d // 2))
-        _need(sin, "sin", torch.float32, (rope_len, d // 2))
+        _is(cos, "cos", torch.float32, (rope_len, d // 2))
+        _is(sin, "sin", torch.float32, (rope_len, d // 2))
     w_dtype = None
     width = (H * d,) if scope == NORM_SCOPE_ALL else (d,)
     for t, name in ((wq, "wq"), (bq, "bq"), (wk, "wk"), (bk, "bk")):
@@ -137,7 +146,7 @@ def qk_norm_rope(q, k=None, wq=None, wk=None, bq=None, bk=None, norm: int = NORM
         w_dtype = w_dtype or t.dtype
         if t.dtype != w_dtype or t.dtype not in (torch.bfloat16, torch.float32):
             raise ValueError(f"{name}: the weights must all be bfloat16 or all float32")
-        _need(t, name, w_dtype, width)
+        _is(t, name, w_dtype, width)
     q_row = 0 if q is None else _rows(q, "q", shape)
     k_row = 0 if k is None else _rows(k, "k", shape)
     if ranks < 0 or (ranks > 0 and H % ranks):
@@ -146,7 +155,7 @@ def qk_norm_rope(q, k=None, wq=None, wk=None, bq=None, bk=None, norm: int = NORM
     for src, t, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
         if src is None and t is not None:
             raise ValueError(f"{name} has no input")
-        _need(t, name, torch.bfloat16, out_shape, optional=True)
+        _is(t, name, torch.bfloat16, out_shape, optional=True)
     dev = _where(stream, "q k wq wk bq bk cos sin q_out k_out", q, k, wq, wk, bq, bk, cos, sin, q_out, k_out)
     if q is not None and q_out is None:
         q_out = _new(out_shape, torch.bfloat16, dev, stream)
@@ -165,7 +174,6 @@ def select_scratch_bytes(B: int, H: int, N: int, d: int) -> int:
 
 def alloc_select_scratch(B: int, H: int, N: int, d: int, device=None):
     """Scratch of select_blocks; calls that may overlap on the GPU need one each."""
-    import torch
     n = select_scratch_bytes(B, H, N, d)
     if n == 0:
         raise SageError(EINVAL, "sage_select_scratch_bytes")
@@ -176,15 +184,14 @@ def select_blocks(q, k, keep: int, first: int = 0, window: int = 0, lists=None, 
     """The `keep` key blocks of every 128-token query block by the scores of pooled queries and keys
     (q, k bf16 [B, H, N, d]); blocks j < first and |i - j| <= window always (window -1: none).
     Returns (lists int32 [B, H, nT, keep] ascending with -1 behind, counts int32 [B, H, nT])."""
-    import torch
     B, H, N, d = sage._bhnd(q, "q")
-    _need(q, "q", torch.bfloat16)
-    _need(k, "k", torch.bfloat16, (B, H, N, d))
+    _is(q, "q", torch.bfloat16, q.shape)
+    _is(k, "k", torch.bfloat16, q.shape)
     if keep < 1:
         raise ValueError("keep must be at least 1")
     nT = (N + BLK - 1) // BLK
-    _need(lists, "lists", torch.int32, (B, H, nT, keep), optional=True)
-    _need(counts, "counts", torch.int32, (B, H, nT), optional=True)
+    _is(lists, "lists", torch.int32, (B, H, nT, keep), optional=True)
+    _is(counts, "counts", torch.int32, (B, H, nT), optional=True)
     _need(scratch, "scratch", torch.uint8, optional=True)
     dev = _where(stream, "q k lists counts scratch", q, k, lists, counts, scratch)
     if scratch is None:
@@ -199,15 +206,16 @@ def select_blocks(q, k, keep: int, first: int = 0, window: int = 0, lists=None, 
 
 
 def _sparse_args(q, k, v, o, lists, counts, workspace):
-    import torch
     B, H, N, d = shape = tuple(sage._bhnd(q, "q"))
-    for name, t in (("q", q), ("k", k), ("v", v), ("o", o)):
-        _need(t, name, torch.bfloat16, shape, optional=name == "o")
+    _is(q, "q", torch.bfloat16, shape)
+    _is(k, "k", torch.bfloat16, shape)
+    _is(v, "v", torch.bfloat16, shape)
+    _is(o, "o", torch.bfloat16, shape, optional=True)
     nT = (N + BLK - 1) // BLK
     _need(lists, "lists", torch.int32)
     if lists.dim() != 4 or lists.shape[3] < 1 or tuple(lists.shape[:3]) != (B, H, nT):
         raise ValueError(f"lists must have shape {(B, H, nT)} + (width,), got {tuple(lists.shape)}")
-    _need(counts, "counts", torch.int32, (B, H, nT))
+    _is(counts, "counts", torch.int32, (B, H, nT))
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     return B, H, N, d
@@ -221,7 +229,6 @@ def attn_fwd_sparse(q, k, v, mode: int, lists, counts, coeff: int = COEFF_DIVIDE
     codes of the dense call) or COEFF_RECIPROCAL (the codes of torch's 127.0 / amax on the GPU).  workspace: sage.alloc_workspace(B, H, N, d, mode); sage.status() on it reports a bad
     index or count (EINVAL).
     """
-    import torch
     B, H, N, d = _sparse_args(q, k, v, o, lists, counts, workspace)
     dev = _where(stream, "q k v o lists counts workspace", q, k, v, o, lists, counts, workspace)
     if o is None:
@@ -237,7 +244,6 @@ def attn_fwd_sparse(q, k, v, mode: int, lists, counts, coeff: int = COEFF_DIVIDE
 
 
 def dbg_sparse_forced_timeout(q, k, v, mode: int, lists, counts, workspace, timeout_cycles: int, stream=None):
-    import torch
     B, H, N, d = _sparse_args(q, k, v, None, lists, counts, workspace)
     dev = _where(stream, "q k v lists counts workspace", q, k, v, lists, counts, workspace)
     o = _new((B, H, N, d), torch.bfloat16, dev, stream)
