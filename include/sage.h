@@ -395,8 +395,9 @@ int sage_ulysses_permute(const void* src, void* dst, int B, int Nl, int H, int d
 /*
  * Reads and clears the device status word at the start of `workspace`
  * (synchronises `stream`).  Returns SAGE_OK, SAGE_ETIMEOUT if a bounded
- * device-side wait ran out since the last call, or SAGE_ELAUNCH if the stream
- * reports a CUDA error.
+ * device-side wait ran out since the last call, SAGE_EINVAL if a call of
+ * sage_attn_fwd_sparse met a block index or count out of range, or
+ * SAGE_ELAUNCH if the stream reports a CUDA error.
  */
 int sage_status(void* workspace, void* stream);
 

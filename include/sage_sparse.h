@@ -56,8 +56,8 @@ extern "C" {
  *           q_out == q (k_out == k) with out_ranks 1 and stride H * d: in place.
  *
  * Arithmetic in fp32, one rounding to bf16.  d 64 or 128, H * d <= 16384, B <=
- * 65535, B * N < 2^31.  Errors: SAGE_EINVAL (sizes, strides, pointers, overlap, arguments that do
- * not belong together), SAGE_EUNSUPPORTED (d, H * d, device).
+ * 65535, B * N < 2^31.  Errors: SAGE_EINVAL (sizes, strides, pointers, overlap,
+ * arguments that do not belong together), SAGE_EUNSUPPORTED (d, H * d, device).
  */
 #define SAGE_NORM_NONE 0
 #define SAGE_NORM_RMS 1
@@ -88,6 +88,7 @@ int sage_qk_norm_rope(const void* q, const void* k, long long q_stride, long lon
  * counts    int32 [B, H, nT]: how many
  * scratch   at least sage_select_scratch_bytes(B, H, N, d) bytes, 16-byte
  *           aligned.  Calls that overlap on the GPU need a scratch each.
+ * lists, counts and scratch must not overlap each other or q and k.
  * nT at most SAGE_SELECT_MAX_BLOCKS (a row of scores stays in shared memory);
  * more is SAGE_EUNSUPPORTED (sage_select_scratch_bytes: 0).  Errors otherwise as
  * sage_quantize_qk.
@@ -106,7 +107,8 @@ int sage_select_blocks(const void* q, const void* k, int B, int H, int N, int d,
  * blocks in ascending order gives the bits of sage_attn_fwd (with
  * SAGE_COEFF_DIVIDE).
  *
- * q, k, v, o  bf16 [B, H, N, d]; o must not overlap the other buffers
+ * q, k, v, o  bf16 [B, H, N, d]; o and the workspace must not overlap each other
+ *           or the other buffers
  * lists     int32 [B, H, nT, width], width >= 1 (sage_select_blocks' keep, or any)
  * counts    int32 [B, H, nT], 0 .. width
  * coeff     how the INT8/FP8 modes round the quantization coefficients scale =
@@ -117,10 +119,12 @@ int sage_select_blocks(const void* q, const void* k, int B, int H, int N, int d,
  *           127.0 / amax (a division by a number, or of one, is a product with a
  *           rounded reciprocal there); a code at a rounding border may differ.
  * workspace as in sage_attn_fwd (sage_workspace_bytes, 256-byte aligned, zero
- *           status word before the first call)
- * The lists are read on the device: an index outside [0, nT) adds nothing, a
- * count outside [0, width] is clamped, and sage_status() on the workspace then
- * returns SAGE_EINVAL.
+ *           status word before the first call).  In every mode calls that overlap
+ *           on the GPU need a workspace each, and so do graphs that are replayed
+ *           at once: the counter that hands out the work lies in it.
+ * The lists are read on the device: an index outside [0, nT) adds nothing,
+ * whatever the tensors hold, a count outside [0, width] is clamped, and
+ * sage_status() on the workspace then returns SAGE_EINVAL.
  */
 #define SAGE_COEFF_DIVIDE 0
 #define SAGE_COEFF_RECIPROCAL 1

@@ -82,15 +82,16 @@ def test_norm_rope_in_place_and_well_formed_calls_reach_the_device_check():
 
 def test_select_refusals():
     f = sage.LIB.sage_select_blocks
-    a, odd = VP(1 << 30), VP((1 << 30) + 8)
+    at, odd = [VP((i + 1) << 30) for i in range(5)], VP((1 << 30) + 8)
     n = sparse.select_scratch_bytes(1, 2, 1000, 128)
     rows = 2 * 2 * 8                     # means, three slices, a step and a norm for every block of q and k
     assert n == rows * 128 * 4 + rows * 3 * 128 + 2 * 256
-    ok = lambda q=a, k=a, B=1, H=2, N=1000, d=128, keep=3, first=0, window=0, li=a, co=a, sc=a, nb=n: f(
+    ok = lambda q=at[0], k=at[1], B=1, H=2, N=1000, d=128, keep=3, first=0, window=0, li=at[2], co=at[3], sc=at[4], nb=n: f(
         q, k, B, H, N, d, keep, first, window, li, co, sc, nb, None)
     for kw in (dict(q=None), dict(k=odd), dict(B=0), dict(N=0), dict(keep=0), dict(first=-1), dict(window=-2),
                dict(window=2), dict(first=3), dict(first=2 ** 31 - 1, window=2 ** 31 - 1), dict(li=None), dict(co=VP(6)),
-               dict(sc=odd), dict(H=70000)):
+               dict(sc=odd), dict(H=70000), dict(li=at[0]), dict(co=at[1]), dict(sc=at[0]), dict(sc=at[1]),
+               dict(co=at[2]), dict(sc=at[2]), dict(sc=at[3]), dict(li=VP((2 << 30) + 511996))):
         assert ok(**kw) == sage.EINVAL, kw
     assert ok(d=96) == sage.EUNSUPPORTED
     assert ok(nb=n - 1) == sage.EWORKSPACE
@@ -100,7 +101,8 @@ def test_select_refusals():
     with pytest.raises(sage.SageError):
         sparse.alloc_select_scratch(1, 1, most + 1, 64)
     if not torch.cuda.is_available():
-        assert ok() in (sage.ELAUNCH, sage.EUNSUPPORTED)
+        for kw in (dict(), dict(k=at[0]), dict(li=VP((2 << 30) + 512000))):           # one tensor as q and k; behind k
+            assert ok(**kw) in (sage.ELAUNCH, sage.EUNSUPPORTED), kw
         assert ok(keep=8, first=9, window=9) in (sage.ELAUNCH, sage.EUNSUPPORTED)     # every block is kept
 
 
@@ -111,14 +113,16 @@ def test_sparse_refusals():
     call = lambda **kw: sage.LIB.sage_attn_fwd_sparse(*{**base, **kw}.values(), None)
     for kw in (dict(q=None), dict(v=(3 << 30) + 8), dict(N=0), dict(mode=3), dict(mode=-1), dict(width=0), dict(coeff=2), dict(coeff=-1), dict(li=None),
                dict(co=(6 << 30) + 2), dict(ws=(7 << 30) + 16), dict(o=1 << 30), dict(o=(2 << 30) + 1024),
-               dict(o=5 << 30), dict(o=6 << 30), dict(o=7 << 30), dict(H=70000)):
+               dict(o=5 << 30), dict(o=6 << 30), dict(o=7 << 30), dict(H=70000), dict(ws=1 << 30), dict(ws=2 << 30),
+               dict(ws=3 << 30), dict(li=(7 << 30) + 4), dict(co=(7 << 30) + n - 4)):
         assert call(**kw) == sage.EINVAL, kw
     assert call(d=32) == sage.EUNSUPPORTED
     assert call(nb=n - 1) == sage.EWORKSPACE
     dbg = lambda cycles: sage.LIB.sage_dbg_sparse_forced_timeout(*base.values(), cycles, None)
     assert dbg(10) == sage.EINVAL and dbg(1 << 60) == sage.EINVAL
     if not torch.cuda.is_available():
-        assert call() in (sage.ELAUNCH, sage.EUNSUPPORTED)
+        for kw in (dict(), dict(k=1 << 30, v=1 << 30), dict(co=(7 << 30) + n)):
+            assert call(**kw) in (sage.ELAUNCH, sage.EUNSUPPORTED), kw
 
 
 def test_binding_refuses_what_the_c_abi_cannot_see():

@@ -365,9 +365,12 @@ int check_sparse(const void* q, const void* k, const void* v, void* o, int B, in
   if (workspace_bytes < sage_workspace_bytes(B, H, N, d, mode)) return SAGE_EWORKSPACE;
   const size_t tensor = (size_t)B * H * N * d * 2, rows = (size_t)B * H * num_tiles(N);
   if (overlap(o, tensor, q, tensor) || overlap(o, tensor, k, tensor) || overlap(o, tensor, v, tensor) ||
-      overlap(o, tensor, lists, rows * width * 4) || overlap(o, tensor, counts, rows * 4) ||
-      overlap(o, tensor, workspace, sage_workspace_bytes(B, H, N, d, mode)))
+      overlap(o, tensor, lists, rows * width * 4) || overlap(o, tensor, counts, rows * 4))
     return SAGE_EINVAL;
+  const size_t ws = sage_workspace_bytes(B, H, N, d, mode);
+  for (const void* p : {q, k, v, (const void*)o})
+    if (overlap(workspace, ws, p, tensor)) return SAGE_EINVAL;
+  if (overlap(workspace, ws, lists, rows * width * 4) || overlap(workspace, ws, counts, rows * 4)) return SAGE_EINVAL;
   return check_device();
 }
 
@@ -459,7 +462,16 @@ int sage_select_blocks(const void* q, const void* k, int B, int H, int N, int d,
   for (const void* p : ptrs)
     if (!p || !aligned16(p)) return SAGE_EINVAL;
   if (!lists || !counts || !aligned4(lists) || !aligned4(counts)) return SAGE_EINVAL;
-  if (scratch_bytes < select_scratch_bytes(B * H, N, d)) return SAGE_EWORKSPACE;
+  const size_t need = select_scratch_bytes(B * H, N, d), tensor = (size_t)B * H * N * d * 2;
+  const size_t rows = (size_t)B * H * nT, list_bytes = rows * keep * 4, count_bytes = rows * 4;
+  if (scratch_bytes < need) return SAGE_EWORKSPACE;
+  for (const void* p : {q, k})
+    if (overlap(p, tensor, lists, list_bytes) || overlap(p, tensor, counts, count_bytes) ||
+        overlap(p, tensor, scratch, need))
+      return SAGE_EINVAL;
+  if (overlap(lists, list_bytes, counts, count_bytes) || overlap(scratch, need, lists, list_bytes) ||
+      overlap(scratch, need, counts, count_bytes))
+    return SAGE_EINVAL;
   if ((rc = check_device()) != SAGE_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return debug_collect(st, launch_status(launch_select_blocks(q, k, B * H, N, d, keep, first, window, lists, counts,

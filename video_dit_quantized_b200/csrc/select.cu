@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kPoolThreads<D>) pool_blocks_kernel(const uint
       if (SAGE_DCHECK(at / 8, ext, kSitePoolIn))
         x = __double2float_rn(t - (double)__bfloat162float(reinterpret_cast<const __nv_bfloat16*>(k)[at]));
     }
-    float sq = mean * mean, am = fabsf(x) < INFINITY ? fabsf(x) : INFINITY;   // not finite: the step becomes inf
+    float sq = mean * mean, am = fabsf(x) < INFINITY ? fabsf(x) : INFINITY;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       sq += __shfl_xor_sync(0xffffffffu, sq, o);
@@ -134,6 +134,9 @@ __global__ void __launch_bounds__(kPoolThreads<D>) pool_blocks_kernel(const uint
       sq += norm_part[i];
       am = fmaxf(am, amax_part[i]);
     }
+    // Not finite, or so small that squares and the reciprocal leave the normal range: an
+    // infinite step, and with it an infinite error bound, sends the rows to the second pass.
+    if (am > 0.f && am < 1e-15f) am = INFINITY;
     const float y = am > 0.f && am < INFINITY ? fminf(fmaxf(x * (127.f / am), -127.f), 127.f) : 0.f;
     const float a0 = rintf(y), r1 = (y - a0) * 128.f, a1 = rintf(r1), a2 = rintf((r1 - a1) * 128.f);
     const long long slice = (long long)gridDim.y * nT * D;             // elements of one slice of one tensor
@@ -524,6 +527,7 @@ __global__ void __launch_bounds__(kScoreThreads, ROWS == kRows ? 2 : 1)
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) sq[r] = i0 + r < nT ? p.pooled.step[qrow + i0 + r] : 0.f;
   bool ok = true;
+  int fetched = 1, committed = 0;                 // thread 0: tiles asked for, tiles given to the tensor cores
   for (int x = 0; x < ntiles; ++x) {
     tc_fence_before();
     if (!__syncthreads_and(ok)) break;            // the accumulators of tile x - 2 are read
@@ -544,6 +548,7 @@ __global__ void __launch_bounds__(kScoreThreads, ROWS == kRows ? 2 : 1)
                               make_sdesc(b + (w - sl) * C::ROW_BYTES + k * 32, 16, 8 * D, C::LAYOUT), kScoreIdesc,
                               sl > 0 || k > 0 ? 1u : 0u);
       mma_commit(&done);
+      ++committed;
     }
     if (x == 0 && warp < 4) {
       // meanwhile: the largest norm and step of the head's keys, for the error bound
@@ -561,7 +566,10 @@ __global__ void __launch_bounds__(kScoreThreads, ROWS == kRows ? 2 : 1)
     }
     ok = __all_sync(0xffffffffu, mbar_wait(&done, x & 1, &gave_up, kDefaultTimeoutCycles) && ok);
     tc_fence_after();
-    if (threadIdx.x == 0 && ok && x + 1 < ntiles) fetch_keys(x + 1);
+    if (threadIdx.x == 0 && ok && x + 1 < ntiles) {
+      fetch_keys(x + 1);
+      ++fetched;
+    }
     if (ok && warp >= 4) {
       // thread = key block, columns = query blocks
       const int j = x * kKeys + threadIdx.x - 128;
@@ -588,6 +596,11 @@ __global__ void __launch_bounds__(kScoreThreads, ROWS == kRows ? 2 : 1)
   }
   for (int j = ntiles * kKeys + threadIdx.x; j < p.nTp; j += kScoreThreads)
     for (int r = 0; r < ROWS; ++r) scores[(size_t)r * p.nTp + j] = -INFINITY;
+  if (threadIdx.x == 0 && gave_up) {              // what is under way ends before its memory is used again
+    volatile int no_abort = 0;
+    mbar_wait(&full, (fetched - 1) & 1, &no_abort, kDefaultTimeoutCycles);
+    if (committed > 0) mbar_wait(&done, (committed - 1) & 1, &no_abort, kDefaultTimeoutCycles);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

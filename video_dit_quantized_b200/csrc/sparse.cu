@@ -86,7 +86,7 @@ struct SparseCfg {
 // What the threads of one lane share.
 template <int KS, int VS>
 struct Lane {
-  float v_scale[2][128];            // QUANT: of the items' heads, alternating
+  float v_scale[2][128];            // QUANT: of the heads of the items with steps, alternating
   Item item[2];
   uint64_t q_full, q_empty;
   uint64_t k_full[KS], k_empty[KS];
@@ -226,17 +226,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto listed = [&](int j) {
           return j < c && SAGE_DCHECK(off + j, (long long)prm.items * prm.width, kSiteSparseList) ? __ldg(prm.lists + off + j) : 0;
         };
-        // an index outside the sequence loads block 0, whose scores the softmax masks
-        auto safe = [&](int x) { return (unsigned)x < (unsigned)nT ? x : 0; };
+        // An index outside the sequence: the softmax masks its scores, and V must be zeros
+        // (0 * inf would not be 0), which are read behind the end of the tensor.
+        auto safe = [&](int x, int otherwise) { return (unsigned)x < (unsigned)nT ? x : otherwise; };
         auto put_k = [&](int x) {
           if (!slot_free(nk, KS, b.k_full, b.k_empty)) return false;
-          load(&tmK, k_dst + (nk % KS) * TILE, &b.k_full[nk % KS], it.bh, safe(x), false);
+          load(&tmK, k_dst + (nk % KS) * TILE, &b.k_full[nk % KS], it.bh, safe(x, 0), false);
           ++nk;
           return true;
         };
         auto put_v = [&](int x) {
           if (!slot_free(nv, VS, b.v_full, b.v_empty)) return false;
-          load(&tmV, v_dst + (nv % VS) * TILE, &b.v_full[nv % VS], it.bh, safe(x), true);
+          load(&tmV, v_dst + (nv % VS) * TILE, &b.v_full[nv % VS], it.bh, safe(x, nT), true);
           ++nv;
           return true;
         };
@@ -373,8 +374,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n = 0; ok; ++n) {
       const int c = it.steps;
       if (c < 0) break;
-      // every thread's value reaches the others through p_full, the MMA thread and o_ready
-      if (QUANT && c > 0 && row < D) b.v_scale[n & 1][row] = vsc;
+      // Every thread's value reaches the others through p_full, the MMA thread and o_ready,
+      // and the item with steps before this one has had all threads past the one before it.
+      if (QUANT && c > 0 && row < D) b.v_scale[done & 1][row] = vsc;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < c; ++j) {
         const int blk = blk_next;
@@ -523,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // with them; where both give the same bf16 that is the result, else divide.
       const float rl = __frcp_rn(l);
       const float rlo = __uint_as_float(__float_as_uint(rl) - 1u), rhi = __uint_as_float(__float_as_uint(rl) + 1u);
-      const float4* vs4 = reinterpret_cast<const float4*>(b.v_scale[n & 1]);
+      const float4* vs4 = reinterpret_cast<const float4*>(b.v_scale[(done - 1) & 1]);
 #pragma unroll
       for (int ch = 0; ch < D / 32; ++ch) {
         uint32_t w[16];

@@ -65,14 +65,16 @@ def _launch(what: str, dev: int, *args):
     _check(rc, what)
 
 
-def _new(shape, dtype, dev: int, stream, zero: bool = False):
-    """Device memory made for one call, of the stream that the call runs on: zeroed there, and not given to
-    anyone else before that stream is done with it."""
-    make = torch.zeros if zero else torch.empty
-    if stream is None:
-        return make(shape, dtype=dtype, device=f"cuda:{dev}")
-    with torch.cuda.stream(stream):
-        return make(shape, dtype=dtype, device=f"cuda:{dev}")
+def _new(shape, dtype, dev: int, stream, zeroed: int = 0):
+    """Device memory made for one call, of the stream that the call runs on: its first elements zeroed there, and
+    not given to anyone else before that stream is done with it."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _new(shape, dtype, dev, None, zeroed)
+    t = torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
+    if zeroed:
+        t[:zeroed].zero_()
+    return t
 
 
 def _is(t, name, dtype, shape, optional=False):
@@ -226,8 +228,9 @@ def attn_fwd_sparse(q, k, v, mode: int, lists, counts, coeff: int = COEFF_DIVIDE
 
     lists int32 [B, H, nT, width], counts int32 [B, H, nT] as select_blocks gives them, or any lists: an empty
     one gives rows of 0.  coeff: how the INT8/FP8 modes round the quantization coefficients, COEFF_DIVIDE (the
-    codes of the dense call) or COEFF_RECIPROCAL (the codes of torch's 127.0 / amax on the GPU).  workspace: sage.alloc_workspace(B, H, N, d, mode); sage.status() on it reports a bad
-    index or count (EINVAL).
+    codes of the dense call) or COEFF_RECIPROCAL (the codes of torch's 127.0 / amax on the GPU).
+    workspace: sage.alloc_workspace(B, H, N, d, mode); sage.status() on it reports a bad index or count (EINVAL),
+    and calls that overlap on the GPU, in BF16 mode too, need one each.
     """
     B, H, N, d = _sparse_args(q, k, v, o, lists, counts, workspace)
     dev = _where(stream, "q k v o lists counts workspace", q, k, v, o, lists, counts, workspace)
@@ -237,7 +240,7 @@ def attn_fwd_sparse(q, k, v, mode: int, lists, counts, coeff: int = COEFF_DIVIDE
         n = sage.workspace_bytes(B, H, N, d, mode)
         if n == 0:
             raise SageError(EINVAL, "sage_workspace_bytes")
-        workspace = _new(n, torch.uint8, dev, stream, zero=True)
+        workspace = _new(n, torch.uint8, dev, stream, zeroed=256)       # the status words
     _launch("sage_attn_fwd_sparse", dev, _p(q), _p(k), _p(v), _p(o), B, H, N, d, int(mode), _p(lists),
             _p(counts), lists.shape[3], int(coeff), _p(workspace), workspace.numel() * workspace.element_size(), _handle(stream, dev))
     return o
