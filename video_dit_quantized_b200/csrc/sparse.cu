@@ -6,8 +6,8 @@
 // The arithmetic is that of the dense kernels (attention.cu), step for step in
 // list order, so a list of all blocks in ascending order gives the dense call's
 // bits.  QUANT: exact int32 S, dequantized; P8 = e4m3(p * 448) through shared
-// memory; O += P8 V8.  BF16: S and O += P V with kind::f16, P over S in tensor
-// memory.
+// memory; O += P8 V8.  BF16: S and O += P V with kind::f16, P in tensor memory
+// (D = 64: beside S, D = 128: over S).
 //
 // Work.  One item is one query block (128 rows) with its list.  A persistent CTA
 // per SM runs two lanes, each with Q, K, V, S, P and O of its own: lists differ
@@ -22,9 +22,16 @@
 //                item's epilogue.
 // One thread per lane and task, each in blocking waits: one thread polling for
 // both lanes added its poll to every step of the BF16 kernel, whose steps are a
-// chain S -> P -> PV -> S (6,000 clocks a step against 4,800).  The two softmax
-// warpgroups take turns on the exponential phase (an mbarrier token, strictly
-// alternating); a lane that has run out of items gives its turns away.
+// chain S -> P -> PV -> S (6,000 clocks a step against 4,800).
+// Where P has a place of its own (QUANT: shared memory; BF16 with D = 64: the
+// tensor memory that the shorter O leaves) the next S is formed while this one is
+// in the softmax: 4,040 clocks for a step of both lanes become 3,630 (BF16, D = 64).
+// The two softmax warpgroups take turns on the exponential phase (an mbarrier
+// token, strictly alternating; a lane that has run out of items gives its turns
+// away), except in BF16 with D = 64.  Clocks for a step of both lanes with and
+// without turns: QUANT 3,770 and 4,220 (D = 64), 3,750 and 4,310 (D = 128); BF16
+// 5,010 and 5,540 (D = 128), but 3,630 and 3,230 (D = 64), where neither the MMAs nor
+// the packing of P hold the other lane up.  2,048 of them are the exponentials.
 // K and V tiles have rings of their own: K_j is free once Q K_j^T is done, a
 // whole step before V_j.
 //
@@ -68,10 +75,10 @@ template <int D, bool QUANT>
 struct SparseCfg {
   using C = Cfg<D, QUANT>;
   static constexpr int TILE_BYTES = C::TILE_BYTES;
-  // K and V slots of each lane
-  // (BF16: a second K slot has no use, QK_j+1 follows PV_j; more shared memory for
-  // rings left less L1 for the lists and cost 3% at d = 64)
-  static constexpr int KS = QUANT ? 2 : 1;
+  static constexpr bool AHEAD = QUANT || D == 64;    // the next S before this step's PV
+  static constexpr bool TURNS = QUANT || D == 128;   // the lanes take turns on the exponentials
+  // K and V slots of each lane (without AHEAD a second K slot has no use, QK_j+1 follows PV_j)
+  static constexpr int KS = AHEAD ? 2 : 1;
   static constexpr int VS = KS;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = 2 * TILE_BYTES;                    // [2][KS]
@@ -92,9 +99,9 @@ struct Lane {
   uint64_t k_full[KS], k_empty[KS];
   uint64_t v_full[VS], v_empty[VS];
   uint64_t s_full;                  // S written (MMA commit)
-  uint64_t s_free;                  // QUANT: S read into registers
+  uint64_t s_free;                  // AHEAD: S read into registers
   uint64_t p_full;                  // P written, O rescaled
-  uint64_t o_ready;                 // QUANT: a PV done; BF16: the item's last PV done
+  uint64_t o_ready;                 // AHEAD: a PV done; else the item's last PV done
   uint64_t tok;                     // this lane's turn on the exponential phase
   uint64_t item_full[2], item_empty[2];
 };
@@ -114,6 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<D, QUANT>;
   using SC = SparseCfg<D, QUANT>;
   constexpr int KS = SC::KS, VS = SC::VS, TILE = SC::TILE_BYTES;
+  constexpr bool AHEAD = SC::AHEAD, TURNS = SC::TURNS;
   using L = Lane<KS, VS>;
   static_assert(sizeof(L) <= SC::LANE_BYTES, "lane struct");
   extern __shared__ uint8_t smem_raw[];
@@ -273,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t v_s = smem_u32(smem + SC::OFF_V + t * VS * TILE);
       const uint32_t p_s = smem_u32(smem + SC::OFF_P + t * C::P_BYTES);
       const uint32_t d_s = tmem + t * 128, d_o = tmem + 256 + t * D;
+      const uint32_t d_p = AHEAD ? tmem + 384 + t * 64 : d_s;   // BF16
       bool ok = true;
       if (prm.dbg_flags & 1) ok = mbar_wait(never, 0, abort_flag, limit);
       int qk = 0, pv = 0, nq = 0;                      // steps issued, Q tiles taken, over all items
@@ -298,8 +307,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // softmax of its last S, is issued
         ok = ok && issue_s(c == 1);
         for (int j = 0; j < c && ok; ++j) {
-          // QUANT: the next S as soon as this one is in the softmax warps' registers
-          if (QUANT && j + 1 < c) ok = mbar_wait(&b.s_free, (qk - 1) & 1, abort_flag, limit) && issue_s(j + 2 == c);
+          // AHEAD: the next S as soon as this one is in the softmax warps' registers
+          if (AHEAD && j + 1 < c) ok = mbar_wait(&b.s_free, (qk - 1) & 1, abort_flag, limit) && issue_s(j + 2 == c);
           ok = ok && mbar_wait(&b.p_full, pv & 1, abort_flag, limit) &&
                mbar_wait(&b.v_full[pv % VS], (pv / VS) & 1, abort_flag, limit);
           // (an item's first PV overwrites O: p_full comes behind the previous epilogue's reads)
@@ -308,12 +317,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (QUANT)
             issue_pv_quant<D>(d_o, p_s, v_s + (pv % VS) * TILE, j > 0 ? 1u : 0u);
           else
-            issue_pv_bf16<D>(d_o, d_s, v_s + (pv % VS) * TILE, j > 0 ? 1u : 0u);
-          if (QUANT || j + 1 == c) mma_commit(&b.o_ready);
+            issue_pv_bf16<D>(d_o, d_p, v_s + (pv % VS) * TILE, j > 0 ? 1u : 0u);
+          if (AHEAD || j + 1 == c) mma_commit(&b.o_ready);
           mma_commit(&b.v_empty[pv % VS]);
           ++pv;
-          // BF16: P lies over S, and operations of one thread execute in order
-          if (!QUANT && j + 1 < c) ok = issue_s(j + 2 == c);
+          // else P lies over S, and operations of one thread execute in order
+          if (!AHEAD && j + 1 < c) ok = issue_s(j + 2 == c);
         }
       }
       // drain: every MMA issued must complete before TMEM is released
@@ -330,11 +339,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t tS = tmem + lane_off + t * 128;
     const uint32_t tO = tmem + lane_off + 256 + t * D;
+    const uint32_t tP = AHEAD ? tmem + lane_off + 384 + t * 64 : tS;   // BF16
     L& b = lane_at(t);
     uint64_t* give = &lane_at(1 - t).tok;
     int step = 0, done = 0;                              // steps (and turns), items with steps so far
     bool ok = true;
-    if (t == 1) mbar_arrive(give);                       // lane 0 has the first turn
+    if (TURNS && t == 1) mbar_arrive(give);              // lane 0 has the first turn
     // int32 S + 0x4B400000 read as a float is 12582912 + S exactly (|S| <= 127*127*128 < 2^22)
     constexpr uint32_t kMagicBits = 0x4B400000u;
     constexpr float kMagic = 12582912.0f;
@@ -395,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) regs_after_wait(*reinterpret_cast<uint32_t(*)[32]>(&sr[ch * 32]));
-        if constexpr (QUANT) {
+        if constexpr (AHEAD) {
           tc_fence_before();
           mbar_arrive(&b.s_free);     // the S columns may now take the next QK
         }
@@ -434,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float m_new = valid > 0 ? fmaxf(m, __fmul_rn(mx, sc)) : m;
         const float alpha = (m == -INFINITY) ? 0.f : ex2_approx(__fsub_rn(m, m_new));
         const float bias = __fsub_rn(kLog2PScale, m_new);   // x = f * sc + bias = s - m_new (+ log2 448)
-        if (!mbar_wait(&b.tok, step & 1, abort_flag, limit)) { ok = false; break; }
+        if (TURNS && !mbar_wait(&b.tok, step & 1, abort_flag, limit)) { ok = false; break; }
         // p = 2^x, row sum (two packed accumulators), P packed for the PV MMA; `mask` zeroes the keys
         // >= N of a last block.  Two copies of the loop, so whole blocks carry no masking at all.
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
@@ -465,13 +475,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int g = 0; g < 32; ++g) group(g, true);
         }
-        mbar_arrive(give);            // hand the exponential phase to the other lane
+        if constexpr (TURNS) mbar_arrive(give);   // hand the exponential phase to the other lane
         const bool grew = j > 0 && __any_sync(0xffffffffu, m_new > m);
+        if (AHEAD && j > 0) {         // the previous PV has read the P tile, O is stable
+          if (!mbar_wait(&b.o_ready, (step - 1) & 1, abort_flag, limit)) { ok = false; break; }
+          tc_fence_after();
+        }
         if constexpr (QUANT) {
-          if (j > 0) {                // the previous PV has read the P tile, O is stable
-            if (!mbar_wait(&b.o_ready, (step - 1) & 1, abort_flag, limit)) { ok = false; break; }
-            tc_fence_after();
-          }
           uint8_t* p_row = smem + SC::OFF_P + t * C::P_BYTES + row * 128;   // this row of the swizzled P tile
 #pragma unroll
           for (int cc = 0; cc < 8; ++cc)
@@ -479,11 +489,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_uint4(pk[4 * cc], pk[4 * cc + 1], pk[4 * cc + 2], pk[4 * cc + 3]);
           fence_proxy_async_smem();   // generic-proxy writes -> visible to the MMA
         } else {
-          tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-          tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[QUANT ? 0 : 32]));
+          tmem_st32(tP, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+          tmem_st32(tP + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[QUANT ? 0 : 32]));
         }
-        // rescale O by alpha where the max grew (BF16: O is complete, the commit after
-        // this step's QK covers the previous PV)
+        // rescale O by alpha where the max grew (without AHEAD O is complete: the commit
+        // after this step's QK covers the previous PV)
         if (grew) {
 #pragma unroll
           for (int ch = 0; ch < D / 32; ++ch) {
@@ -514,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long orow = ((long long)it.bh * N + gq) * D;
       if (!(ok = take_item(n + 1))) break;
       if (c > 0) {
-        if (!mbar_wait(&b.o_ready, (QUANT ? step - 1 : done) & 1, abort_flag, limit)) { ok = false; break; }
+        if (!mbar_wait(&b.o_ready, (AHEAD ? step - 1 : done) & 1, abort_flag, limit)) { ok = false; break; }
         ++done;
         tc_fence_after();
       }
@@ -577,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // A lane without items keeps giving its turns away until the other has ended, too.
     idle[t] = 1;
-    while (ok && !idle[1 - t]) {
+    while (TURNS && ok && !idle[1 - t]) {
       const long long t0 = clock64();
       while (!mbar_try_wait(&b.tok, step & 1) && !idle[1 - t] && ok) {
         if (clock64() - t0 > limit) *abort_flag = 1;
