@@ -177,22 +177,29 @@ __device__ __forceinline__ double exact_score(const float* __restrict__ q, const
   return s;
 }
 
-// The same by a warp, four (D = 64: two) channels a lane and a fixed tree: equal means
-// give equal scores here, too.
+// The same by eight lanes, D / 8 channels each (q: this lane's) and a fixed tree: equal
+// means give equal scores here, too.
 template <int D>
-__device__ __forceinline__ double exact_score_warp(const float* __restrict__ q, const float* __restrict__ k, int lane) {
+__device__ __forceinline__ double exact_score_lanes(const float4 (&q)[D / 32], const float* __restrict__ k, int lane) {
   double s = 0.0;
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c) s = fma((double)q[c * 32 + lane], (double)k[c * 32 + lane], s);
+  for (int c = 0; c < D / 32; ++c) {
+    const float4 b = *reinterpret_cast<const float4*>(k + c * 32 + (lane & 7) * 4);
+    s = fma((double)q[c].x, (double)b.x, s);
+    s = fma((double)q[c].y, (double)b.y, s);
+    s = fma((double)q[c].z, (double)b.z, s);
+    s = fma((double)q[c].w, (double)b.w, s);
+  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
 }
 
 constexpr int kScoreThreads = 256;
+constexpr int kRowRegs = 5;                // float4 of a row that a lane holds in registers
 constexpr int kKeys = 128;                 // key blocks of one tile: the MMA's M
 constexpr int kRows = 16;                  // query blocks of one tile: its N
-constexpr uint32_t kScoreIdesc = make_idesc(kFmtS32Acc, kFmtS8, kFmtS8, 0, kKeys, kRows);
+__host__ __device__ constexpr uint32_t score_idesc(int slices) { return make_idesc(kFmtS32Acc, kFmtS8, kFmtS8, 0, kKeys, slices * kRows); }
 // Shared memory: 3 slices of a key tile (in the second pass: a row of 64-bit scores),
 // 3 slices of the query tile, the fp32 scores of ROWS <= 16 rows.
 template <int D>
@@ -204,15 +211,14 @@ struct ScoreCfg {
   static_assert(8 * SAGE_SELECT_MAX_BLOCKS <= OFF_Q, "the second pass's row must fit");
 };
 
+// Smallest and largest of a warp's floats (no NaN) by the integer reductions: the bits
+// of a negative float, all but the sign inverted, follow integer order, and back.
+__device__ __forceinline__ int int_order(int bits) { return bits ^ (bits >> 31 & 0x7FFFFFFF); }
 __device__ __forceinline__ float warp_min(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fminf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+  return __int_as_float(int_order(__reduce_min_sync(0xffffffffu, int_order(__float_as_int(v)))));
 }
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+  return __int_as_float(int_order(__reduce_max_sync(0xffffffffu, int_order(__float_as_int(v)))));
 }
 
 struct SelectParams {
@@ -245,31 +251,55 @@ __device__ __forceinline__ unsigned mask4(const float4& v, F pred) {
   return (pred(v.x) ? 1u : 0u) | (pred(v.y) ? 2u : 0u) | (pred(v.z) ? 4u : 0u) | (pred(v.w) ? 8u : 0u);
 }
 
-// Writes one row's list by a warp.  make() gives a function of j0 that returns the mask
-// of the kept blocks among j0 .. j0 + 3, called for a lane's stretch in order; it is
-// made twice, to count and to write.
-template <typename F>
-__device__ __forceinline__ void write_list(const SelectParams& p, int bh, int i, int lane, F make) {
-  const long long row = ((long long)bh * p.nT + i) * p.keep, ext = (long long)gridDim.y * p.nT * p.keep;
-  (void)ext;
-  const int from = lane * (p.nTp / 32), to = from + p.nTp / 32;
-  int c = 0;
-  auto counted = make();
-  for (int j0 = from; j0 < to; j0 += 4) c += __popc(counted(j0));
-  int at = lane_prefix(c, lane);
-  const int done = __shfl_sync(0xffffffffu, at + c, 31);
-  auto written = make();
-  for (int j0 = from; j0 < to; j0 += 4) {
-    unsigned m = written(j0);
+// One row's list as a warp writes it: each lane the blocks of its stretch, behind those of
+// the lanes before it.
+struct ListOut {
+  const SelectParams& p;
+  long long row, ext, count;
+  int at, done;
+  __device__ __forceinline__ ListOut(const SelectParams& p_, int bh, int i)
+      : p(p_), row(((long long)bh * p_.nT + i) * p_.keep), ext((long long)gridDim.y * p_.nT * p_.keep),
+        count((long long)bh * p_.nT + i) {}
+  __device__ __forceinline__ void start(int c, int lane) {
+    at = lane_prefix(c, lane);
+    done = __shfl_sync(0xffffffffu, at + c, 31);
+  }
+  __device__ __forceinline__ void put(unsigned m, int j0) {
     while (m) {
       if (at < p.keep && SAGE_DCHECK(row + at, ext, kSiteSelectOut)) p.lists[row + at] = j0 + __ffs(m) - 1;
       ++at;
       m &= m - 1;
     }
   }
-  for (int s = done + lane; s < p.keep; s += 32)
-    if (SAGE_DCHECK(row + s, ext, kSiteSelectOut)) p.lists[row + s] = -1;
-  if (lane == 0) p.counts[(long long)bh * p.nT + i] = done;
+  __device__ __forceinline__ void end(int lane) {
+    for (int s = done + lane; s < p.keep; s += 32)
+      if (SAGE_DCHECK(row + s, ext, kSiteSelectOut)) p.lists[row + s] = -1;
+    if (lane == 0) p.counts[count] = done;
+  }
+};
+
+// Writes one row's list by a warp.  make() gives a function of j0 that returns the mask
+// of the kept blocks among j0 .. j0 + 3, called for a lane's stretch in order; it is
+// made twice, to count and to write.
+template <typename F>
+__device__ __forceinline__ void write_list(const SelectParams& p, int bh, int i, int lane, F make) {
+  ListOut out(p, bh, i);
+  const int from = lane * (p.nTp / 32), to = from + p.nTp / 32;
+  int c = 0;
+  auto counted = make();
+  for (int j0 = from; j0 < to; j0 += 4) c += __popc(counted(j0));
+  out.start(c, lane);
+  auto written = make();
+  for (int j0 = from; j0 < to; j0 += 4) out.put(written(j0), j0);
+  out.end(lane);
+}
+
+// The same for stretches of at most 32 blocks, block j0 + e of a lane kept where bit e of m is set.
+__device__ __forceinline__ void write_bits(const SelectParams& p, int bh, int i, int lane, int j0, unsigned m) {
+  ListOut out(p, bh, i);
+  out.start(__popc(m), lane);
+  out.put(m, j0);
+  out.end(lane);
 }
 
 // One row from its 64-bit ordered scores (two arrays of halves), by one warp.  The
@@ -330,37 +360,78 @@ __device__ __noinline__ void select_exact(const SelectParams& p, int bh, int i, 
   });
 }
 
+// A row's scores as a warp goes through them, lane by lane its stretch of nv float4.
+// NV > 0: held in registers (-inf behind the stretch); 0: read from shared memory.
+template <int NV>
+struct Row {
+  const float4* s4;
+  int nv;
+  float4 v[NV > 0 ? NV : 1];
+  __device__ __forceinline__ Row(const float* s, int lane, int nv_) : s4(reinterpret_cast<const float4*>(s) + lane * nv_), nv(nv_) {
+    if constexpr (NV > 0) {
+#pragma unroll
+      for (int x = 0; x < NV; ++x) v[x] = x < nv ? s4[x] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    }
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    if constexpr (NV > 0) {
+#pragma unroll
+      for (int x = 0; x < NV; ++x) f(x, v[x]);
+    } else {
+#pragma unroll 4
+      for (int x = 0; x < nv; ++x) f(x, s4[x]);
+    }
+  }
+};
+
+// Writes a row's list; make() as in write_list, its function taking (x, scores).
+template <int NV, typename F>
+__device__ __forceinline__ void write_row(const SelectParams& p, int bh, int i, int lane, const Row<NV>& row, F make) {
+  if constexpr (NV > 0) {
+    static_assert(4 * NV <= 32, "a lane's stretch as the bits of one word");
+    unsigned m = 0;
+    auto kept = make();
+    row.each([&](int x, const float4& v) { m |= kept(x, v) << (4 * x); });
+    write_bits(p, bh, i, lane, lane * row.nv * 4, m);
+  } else {
+    write_list(p, bh, i, lane, [&] {
+      return [&, kept = make()](int j0) mutable {
+        const int x = j0 / 4 - lane * row.nv;
+        return kept(x, row.s4[x]);
+      };
+    });
+  }
+}
+
 // One row from its fp32 scores (forced blocks +inf, -inf behind the last), by one
 // warp; false: the order at the border is open among more than 32 blocks.  cand: 32
 // integers of the warp's own.
-template <int D>
+template <int D, int NV>
 __device__ __forceinline__ bool select_row(const SelectParams& p, int bh, int i, int lane, const float* s, float E,
                                            const float* qrow, const float* kp, int* cand) {
   const int nT = p.nT, n = min(p.keep, nT), nv = p.nTp / 128;
-  const float4* s4 = reinterpret_cast<const float4*>(s) + lane * nv;
-  auto load4 = [&](int j0) { return *reinterpret_cast<const float4*>(s + j0); };
+  const Row<NV> row(s, lane, nv);
   if (n == nT) {
-    write_list(p, bh, i, lane, [&] {
-      return [&](int j0) { return j0 + 3 < nT ? 15u : j0 < nT ? (1u << (nT - j0)) - 1u : 0u; };
+    write_row<NV>(p, bh, i, lane, row, [&] {
+      return [&](int x, const float4&) {
+        const int j0 = (lane * nv + x) * 4;
+        return x >= nv || j0 >= nT ? 0u : j0 + 3 < nT ? 15u : (1u << (nT - j0)) - 1u;
+      };
     });
     return true;
   }
   // blocks with a score of at least t
   auto count = [&](float t) {
     float c = 0.f;
-#pragma unroll 4
-    for (int x = 0; x < nv; ++x) {
-      const float4 v = s4[x];
+    row.each([&](int, const float4& v) {
       c += (v.x >= t ? 1.f : 0.f) + (v.y >= t ? 1.f : 0.f);
       c += (v.z >= t ? 1.f : 0.f) + (v.w >= t ? 1.f : 0.f);
-    }
+    });
     return __reduce_add_sync(0xffffffffu, (int)c);
   };
   float mn = INFINITY, mx = -INFINITY, sum = 0.f, sq = 0.f;
-  int forced = 0;
-#pragma unroll 4
-  for (int x = 0; x < nv; ++x) {
-    const float4 v = s4[x];
+  row.each([&](int, const float4& v) {
     const float y[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -369,9 +440,8 @@ __device__ __forceinline__ bool select_row(const SelectParams& p, int bh, int i,
       mx = fmaxf(mx, in ? y[e] : -INFINITY);
       sum += in ? y[e] : 0.f;
       sq += in ? y[e] * y[e] : 0.f;
-      forced += y[e] == INFINITY ? 1 : 0;
     }
-  }
+  });
   mn = warp_min(mn);
   mx = warp_max(mx);
 #pragma unroll
@@ -379,7 +449,8 @@ __device__ __forceinline__ bool select_row(const SelectParams& p, int bh, int i,
     sum += __shfl_xor_sync(0xffffffffu, sum, o);
     sq += __shfl_xor_sync(0xffffffffu, sq, o);
   }
-  forced = __reduce_add_sync(0xffffffffu, forced);
+  const int head = min(p.first, nT);
+  const int forced = head + (p.window < 0 ? 0 : max(0, min(nT - 1, i + p.window) - max(head, i - p.window) + 1));
   // A threshold with count(s >= lo) > n > count(s >= hi) around it.  The first steps are
   // Newton's on a normal distribution of the row's mean and width, which meets n in about
   // five steps where halving takes eleven; from the eighth step on the bracket is halved, so
@@ -409,48 +480,50 @@ __device__ __forceinline__ bool select_row(const SelectParams& p, int bh, int i,
   // a: the smallest kept, b: the largest left out (where no threshold was found, b >= a)
   const float split = found ? T : hi;
   float a = INFINITY, b = -INFINITY;
-#pragma unroll 4
-  for (int x = 0; x < nv; ++x) {
-    const float4 v = s4[x];
+  row.each([&](int, const float4& v) {
     const float y[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       a = fminf(a, y[e] >= split ? y[e] : INFINITY);
       b = fmaxf(b, y[e] >= split ? -INFINITY : y[e]);
     }
-  }
+  });
   b = warp_max(b);
   a = found ? warp_min(a) : lo;
   if (found && a - b > 2.f * E) {
-    write_list(p, bh, i, lane, [&] { return [&](int j0) { return mask4(load4(j0), [&](float v) { return v >= T; }); }; });
+    write_row<NV>(p, bh, i, lane, row, [&] { return [&](int, const float4& v) { return mask4(v, [&](float y) { return y >= T; }); }; });
     return true;
   }
   const float from = a - 2.f * E, to = b + 2.f * E;
   auto is_open = [&](float v) { return v >= from && v <= to; };
   int above = 0, mine = 0;
-  for (int x = 0; x < nv; ++x) {
-    above += __popc(mask4(s4[x], [&](float v) { return v > to; }));
-    mine += __popc(mask4(s4[x], is_open));
-  }
+  row.each([&](int, const float4& v) {
+    above += __popc(mask4(v, [&](float y) { return y > to; }));
+    mine += __popc(mask4(v, is_open));
+  });
   above = __reduce_add_sync(0xffffffffu, above);
   const int open = __reduce_add_sync(0xffffffffu, mine);
   if (open > 32) return false;
   // lane r gets the r-th open block's score in fp64
   const int before = lane_prefix(mine, lane);    // open blocks in front of this lane's stretch
   int at = before;
-  for (int x = 0; x < nv; ++x) {
-    unsigned m = mask4(s4[x], is_open);
+  row.each([&](int x, const float4& v) {
+    unsigned m = mask4(v, is_open);
     while (m) {
       cand[at++] = (lane * nv + x) * 4 + __ffs(m) - 1;
       m &= m - 1;
     }
-  }
+  });
   __syncwarp();
+  // four at a time, eight lanes each
   double v = -INFINITY;
-#pragma unroll 4
-  for (int r = 0; r < open; ++r) {
-    const double x = exact_score_warp<D>(qrow, kp + (size_t)cand[r] * D, lane);
-    if (lane == r) v = x;
+  float4 qv[D / 32];
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) qv[c] = *reinterpret_cast<const float4*>(qrow + c * 32 + (lane & 7) * 4);
+  for (int r = 0; r < open; r += 4) {
+    const double x = exact_score_lanes<D>(qv, kp + (size_t)cand[min(r + (lane >> 3), open - 1)] * D, lane);
+    const double y = __shfl_sync(0xffffffffu, x, (lane & 3) * 8);
+    if (lane >= r && lane < min(r + 4, open)) v = y;
   }
   int rank = 0;
   for (int r = 0; r < open; ++r) {
@@ -458,9 +531,8 @@ __device__ __forceinline__ bool select_row(const SelectParams& p, int bh, int i,
     rank += o > v || (o == v && r < lane) ? 1 : 0;
   }
   const unsigned kept = __ballot_sync(0xffffffffu, lane < open && rank < n - above);
-  write_list(p, bh, i, lane, [&] {
-    return [&, r = before](int j0) mutable {
-      const float4 y = load4(j0);
+  write_row<NV>(p, bh, i, lane, row, [&] {
+    return [&, r = before](int, const float4& y) mutable {
       const unsigned m = mask4(y, is_open);
       unsigned take = mask4(y, [&](float u) { return u > to; });
 #pragma unroll
@@ -473,7 +545,7 @@ __device__ __forceinline__ bool select_row(const SelectParams& p, int bh, int i,
 }
 
 // grid (ceil(nT / ROWS), BH)
-template <int D, int ROWS>
+template <int D, int ROWS, int NV>
 __global__ void __launch_bounds__(kScoreThreads, ROWS == kRows ? 2 : 1)
     score_select_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ,
                         const SelectParams p) {
@@ -503,7 +575,7 @@ __global__ void __launch_bounds__(kScoreThreads, ROWS == kRows ? 2 : 1)
       tma_load_2d(sm + sl * C::KEY_BYTES, &tmK, &full, 0, ((3 + sl) * (int)gridDim.y + bh) * nT + x * kKeys);
   };
   if (warp == 1) {
-    tmem_alloc(&tmem_slot, 128);                   // two sets of accumulators
+    tmem_alloc(&tmem_slot, 64);
     tmem_relinquish();
   }
   if (threadIdx.x == 0) {
@@ -522,46 +594,49 @@ __global__ void __launch_bounds__(kScoreThreads, ROWS == kRows ? 2 : 1)
     for (int sl = 0; sl < 3; ++sl)
       tma_load_2d(sm + C::OFF_Q + sl * C::ROW_BYTES, &tmQ, &full, 0, (sl * (int)gridDim.y + bh) * nT + i0);
   }
-  if (threadIdx.x < kRows) later[threadIdx.x] = 0;
-  float sq[ROWS];
+  // each half of the block turns the accumulators into scores for half the rows
+  constexpr int RH = ROWS / 2;
+  const int r0 = warp < 4 ? 0 : RH;
+  float sq[RH];
 #pragma unroll
-  for (int r = 0; r < ROWS; ++r) sq[r] = i0 + r < nT ? p.pooled.step[qrow + i0 + r] : 0.f;
+  for (int r = 0; r < RH; ++r) sq[r] = i0 + r0 + r < nT ? p.pooled.step[qrow + i0 + r0 + r] : 0.f;
   bool ok = true;
   int fetched = 1, committed = 0;                 // thread 0: tiles asked for, tiles given to the tensor cores
   for (int x = 0; x < ntiles; ++x) {
     tc_fence_before();
-    if (!__syncthreads_and(ok)) break;            // the accumulators of tile x - 2 are read
+    if (!__syncthreads_and(ok)) break;            // the accumulators are read
     tc_fence_after();
-    const uint32_t tmem = tmem_slot + (x & 1) * 64;
+    const uint32_t tmem = tmem_slot;
+    const int j = x * kKeys + (threadIdx.x & 127);            // this thread's key block
+    const float sk = j < nT ? p.pooled.step[krow + j] : 0.f;
     if (threadIdx.x == 0) {
       ok = mbar_wait(&full, x & 1, &gave_up, kDefaultTimeoutCycles);
       tc_fence_after();
       const uint32_t a = smem_u32(sm), b = smem_u32(sm + C::OFF_Q);
+      // Key slice sl times query slices 0 .. 2 - sl, side by side as the columns of one product: accumulator
+      // w, of weight 2^-7w, collects those with sl + query slice = w.
       if (ok)
 #pragma unroll
-        for (int w = 0; w < 3; ++w)               // accumulator of weight 2^-7w
+        for (int sl = 0; sl < 3; ++sl)
 #pragma unroll
-          for (int sl = 0; sl <= w; ++sl)         // key slice sl, query slice w - sl
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k)
-              mma_ss<kKindI8>(tmem + w * kRows, make_sdesc(a + sl * C::KEY_BYTES + k * 32, 16, 8 * D, C::LAYOUT),
-                              make_sdesc(b + (w - sl) * C::ROW_BYTES + k * 32, 16, 8 * D, C::LAYOUT), kScoreIdesc,
-                              sl > 0 || k > 0 ? 1u : 0u);
+          for (int k = 0; k < D / 32; ++k)
+            mma_ss<kKindI8>(tmem + sl * kRows, make_sdesc(a + sl * C::KEY_BYTES + k * 32, 16, 8 * D, C::LAYOUT),
+                            make_sdesc(b + k * 32, 16, 8 * D, C::LAYOUT), score_idesc(3 - sl), sl > 0 || k > 0 ? 1u : 0u);
       mma_commit(&done);
       ++committed;
     }
-    if (x == 0 && warp < 4) {
+    if (x == 0 && warp >= 4) {
       // meanwhile: the largest norm and step of the head's keys, for the error bound
       float kn = 0.f, ks = 0.f;
-      for (int j = threadIdx.x; j < nT; j += 128) {
+      for (int j = threadIdx.x - 128; j < nT; j += 128) {
         kn = fmaxf(kn, p.pooled.norm[krow + j]);
         ks = fmaxf(ks, p.pooled.step[krow + j]);
       }
       kn = warp_max(kn);
       ks = warp_max(ks);
       if (lane == 0) {
-        kmax_part[0][warp] = kn;
-        kmax_part[1][warp] = ks;
+        kmax_part[0][warp - 4] = kn;
+        kmax_part[1][warp - 4] = ks;
       }
     }
     ok = __all_sync(0xffffffffu, mbar_wait(&done, x & 1, &gave_up, kDefaultTimeoutCycles) && ok);
@@ -570,27 +645,28 @@ __global__ void __launch_bounds__(kScoreThreads, ROWS == kRows ? 2 : 1)
       fetch_keys(x + 1);
       ++fetched;
     }
-    if (ok && warp >= 4) {
-      // thread = key block, columns = query blocks
-      const int j = x * kKeys + threadIdx.x - 128;
-      const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-      uint32_t l0[16], l1[16], l2[16];
-      tmem_ld16(at, l0);
-      tmem_ld16(at + kRows, l1);
-      tmem_ld16(at + 2 * kRows, l2);
-      const float sk = j < nT ? p.pooled.step[krow + j] : 0.f;
-      tmem_wait_ld_regs16(l0);
-      tmem_wait_ld_regs16(l1);
-      tmem_wait_ld_regs16(l2);
+    if (ok) {
+      const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + r0;
+      uint32_t l0[8], l1[8], l2[8];
+      tmem_ld8(at, l0);
+      tmem_ld8(at + kRows, l1);
+      tmem_ld8(at + 2 * kRows, l2);
+      tmem_wait_ld_regs8(l0);
+      tmem_wait_ld_regs8(l1);
+      tmem_wait_ld_regs8(l2);
+      float* to = scores + (size_t)r0 * p.nTp + j;
       if (j < p.nTp)
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-          // the sums are exact in fp32 (below 2^22)
-          const float v = fmaf(fmaf((float)(int)l2[r], 0.0078125f, (float)(int)l1[r]), 0.0078125f, (float)(int)l0[r]) *
-                          (sq[r] * sk);
-          const bool forced = j < nT && p.forced(i0 + r, j);
-          if (j < nT && !forced && !(fabsf(v) < INFINITY)) later[r] = 1;
-          scores[(size_t)r * p.nTp + j] = j >= nT ? -INFINITY : forced ? INFINITY : v;
+        for (int r = 0; r < RH; r += 2) {
+          // l0 (below 2^21) as a float by way of 12582912 + l0, whose bits are an integer sum
+          constexpr float kMagic = 12582912.f;
+          const float2 h = fadd2(make_float2(__uint_as_float(l0[r] + 0x4B400000u), __uint_as_float(l0[r + 1] + 0x4B400000u)),
+                                 make_float2(-kMagic, -kMagic));
+          const float2 m = make_float2((float)((int)l1[r] * 128 + (int)l2[r]), (float)((int)l1[r + 1] * 128 + (int)l2[r + 1]));
+          const float2 v = fmul2v(ffma2v(m, make_float2(0x1p-14f, 0x1p-14f), h),
+                                  fmul2v(make_float2(sq[r], sq[r + 1]), make_float2(sk, sk)));
+          to[(size_t)r * p.nTp] = j < nT ? v.x : -INFINITY;
+          to[(size_t)(r + 1) * p.nTp] = j < nT ? v.y : -INFINITY;
         }
     }
   }
@@ -604,7 +680,7 @@ __global__ void __launch_bounds__(kScoreThreads, ROWS == kRows ? 2 : 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem_slot, 128);
+  if (warp == 1) tmem_dealloc(tmem_slot, 64);
   float kn = kmax_part[0][0], ks = kmax_part[1][0];
 #pragma unroll
   for (int w = 1; w < 4; ++w) {
@@ -618,8 +694,13 @@ __global__ void __launch_bounds__(kScoreThreads, ROWS == kRows ? 2 : 1)
     const int i = i0 + rr;
     if (i >= nT) continue;
     const float E = 3.f * p.pooled.step[qrow + i] * ks + 1.1920929e-7f * p.pooled.norm[qrow + i] * kn + 1e-37f;
-    const bool sure = usable && later[rr] == 0 && E < 1e37f &&
-                      select_row<D>(p, bh, i, lane, scores + (size_t)rr * p.nTp, E, qp + (size_t)i * D, kp, cand[warp]);
+    float* row = scores + (size_t)rr * p.nTp;
+    for (int j = lane; j < min(p.first, nT); j += 32) row[j] = INFINITY;
+    for (int j = max(0, i - p.window) + lane; j <= min(nT - 1, i + p.window); j += 32) row[j] = INFINITY;
+    __syncwarp();
+    // below this limit on E, steps and scores are finite
+    const bool sure = usable && E < 1e31f &&
+                      select_row<D, NV>(p, bh, i, lane, row, E, qp + (size_t)i * D, kp, cand[warp]);
     __syncwarp();
     if (lane == 0) later[rr] = sure ? 0 : 1;
   }
@@ -642,7 +723,7 @@ __global__ void __launch_bounds__(kScoreThreads, ROWS == kRows ? 2 : 1)
   }
 }
 
-template <int D, int ROWS>
+template <int D, int ROWS, int NV>
 cudaError_t score_launch(const SelectParams& p, int BH, cudaStream_t stream) {
   alignas(64) CUtensorMap tk, tq;
   const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
@@ -650,7 +731,7 @@ cudaError_t score_launch(const SelectParams& p, int BH, cudaStream_t stream) {
   if (!encode_tmap_2d(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.pooled.slices, D, rows, D, D, kKeys, sw) ||
       !encode_tmap_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.pooled.slices, D, rows, D, D, kRows, sw))
     return cudaErrorInvalidValue;
-  auto kern = score_select_kernel<D, ROWS>;
+  auto kern = score_select_kernel<D, ROWS, NV>;
   const int smem = (int)ScoreCfg<D>::smem(ROWS, p.nTp);
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -705,10 +786,13 @@ cudaError_t select_d(const void* q, const void* k, int BH, int N, int keep, int 
   }
   const float slope = (float)std::max(1.0, nT * std::exp(-0.5 * z * z) / 2.5066282746310002);
   const int nTp = ((nT + 127) / 128 | 1) * 128;
-  const SelectParams p{pooled, nT, nTp, keep, first, window, (float)z, slope, lists, counts};
-  // sixteen rows a CTA, two CTAs per SM, while their scores fit; four for longer rows
-  if (ScoreCfg<D>::smem(kRows, nTp) <= kSmemMax) return score_launch<D, kRows>(p, BH, stream);
-  return score_launch<D, 4>(p, BH, stream);
+  const SelectParams p{pooled, nT, nTp, keep, first, std::min(window, nT), (float)z, slope, lists, counts};
+  // a warp's row in registers while a lane's stretch is at most 20 blocks (row read again for
+  // every threshold: @@ us at 1 x 40 x 75600 x 128, in registers @@); sixteen rows a CTA, two
+  // CTAs per SM, while their scores fit; four for longer rows
+  if (nTp <= 128 * kRowRegs) return score_launch<D, kRows, kRowRegs>(p, BH, stream);
+  if (ScoreCfg<D>::smem(kRows, nTp) <= kSmemMax) return score_launch<D, kRows, 0>(p, BH, stream);
+  return score_launch<D, 4, 0>(p, BH, stream);
 }
 
 }  // namespace
