@@ -14,7 +14,7 @@
 //   x = step * (a0 + a1 / 2^7 + a2 / 2^14) + r,   step = amax / 127,   |r| <= 2^-14 step,
 // and the six products of weight up to 2^-14 are summed in int32 (tcgen05 kind::i8,
 // one accumulator a weight).  (All scores in fp64: 864 us at 1 x 40 x 75600 x 128; in
-// fp32 on the FMA pipe, bound by shared-memory wavefronts: 247 us.)  Of the keys,
+// fp32 on the FMA pipe, bound by shared-memory wavefronts: 247 us; so: 98 us.)  Of the keys,
 // token 0's values are subtracted first, which shifts a row's scores alike and
 // makes amax, and with it the error, small where channels carry an offset.
 //
@@ -22,11 +22,17 @@
 // read once; it writes the means, their slices, steps and norms.  score: one CTA
 // per (16 query blocks, head) forms its rows of scores against every key block of
 // the head in shared memory (the score matrix never reaches HBM), then one warp per
-// row looks for a threshold with n scores at or above it.
+// row looks for a threshold with n scores at or above it.  What bounds it: latency (two
+// CTAs of 8 warps per SM by shared memory); of 30,000 clocks a CTA the tiles take 14,000,
+// a third of it the products' reads of the key slices from shared memory (each slice is
+// read once for all query slices: the products took twice as long with one each), and
+// a row's selection 5,000, 13,000 where scores are refined.
+// The call at 1 x 40 x 75600 x 128: 360 us (4.3 TB/s), the pool kernel of it 262 (5.9 TB/s,
+// 0.90 of a copy); 1 x 30 x 17776 x 64: 44 us.
 //   |computed - exact| <= E = 3 step_q max step_k + 2^-23 |qbar| max |kbar|:
 //   the products left out are below 0.51 step_q step_k (128 * 2 * 64 * 64 * 2^-21), the
-//   remainders r below 128 * 127 * 2 * 4.7e-5 = 1.53, six fp32 roundings of at most
-//   2.1e6 below 0.75, that of kbar - token 0 below 0.13; the second term is the rounding
+//   remainders r below 128 * 127 * 2 * 4.7e-5 = 1.53, four fp32 roundings of at most
+//   2.1e6 below 0.5, that of kbar - token 0 below 0.13; the second term is the rounding
 //   of kbar in the definition.
 //   a = the smallest kept, b = the largest left out: a - b > 2 E decides the row.
 //   Else the rows' order is open only among scores in [a - 2 E, b + 2 E]: up to 32 of
@@ -787,9 +793,9 @@ cudaError_t select_d(const void* q, const void* k, int BH, int N, int keep, int 
   const float slope = (float)std::max(1.0, nT * std::exp(-0.5 * z * z) / 2.5066282746310002);
   const int nTp = ((nT + 127) / 128 | 1) * 128;
   const SelectParams p{pooled, nT, nTp, keep, first, std::min(window, nT), (float)z, slope, lists, counts};
-  // a warp's row in registers while a lane's stretch is at most 20 blocks (row read again for
-  // every threshold: @@ us at 1 x 40 x 75600 x 128, in registers @@); sixteen rows a CTA, two
-  // CTAs per SM, while their scores fit; four for longer rows
+  // A warp's row in registers while a lane's stretch is at most 20 blocks (read again for
+  // every threshold the call takes 401 us at 1 x 40 x 75600 x 128, in registers 375);
+  // sixteen rows a CTA, two CTAs per SM, while their scores fit; four for longer rows.
   if (nTp <= 128 * kRowRegs) return score_launch<D, kRows, kRowRegs>(p, BH, stream);
   if (ScoreCfg<D>::smem(kRows, nTp) <= kSmemMax) return score_launch<D, kRows, 0>(p, BH, stream);
   return score_launch<D, 4, 0>(p, BH, stream);
