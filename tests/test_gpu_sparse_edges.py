@@ -42,6 +42,13 @@ def test_block_scores_with_infinite_tokens(cuda_dev):
         check_select(q, k, 4, 0, -1)
 
 
+@pytest.mark.parametrize("nT,d,keep", [(128, 64, 12), (129, 128, 128), (640, 64, 64), (641, 128, 1), (641, 64, 640)])
+def test_block_rows_at_the_borders_of_their_forms(nT, d, keep, cuda_dev):
+    """Rows that just fit a lane's registers or a power of blocks, and one more; lists that keep one and all but one."""
+    q, k = (draw((1, 1, nT * 128 - 77, d), s, cuda_dev) for s in (17, 18))
+    check_select(q, k, keep, 0, -1)
+
+
 @pytest.mark.parametrize("mode", [BF16, I8, QTOK])
 @pytest.mark.parametrize("value", [math.inf, math.nan])
 def test_a_bad_index_adds_nothing_whatever_block_0_holds(mode, value, cuda_dev):
