@@ -65,13 +65,13 @@ def _launch(what: str, dev: int, *args):
     _check(rc, what)
 
 
-def _new(shape, dtype, dev: int, stream, zeroed: int = 0):
-    """Device memory made for one call, of the stream that the call runs on: its first elements zeroed there, and
-    not given to anyone else before that stream is done with it."""
+def _new(like, shape, dtype, stream, zeroed: int = 0):
+    """Memory on the device of `like` made for one call, of the stream that the call runs on: its first elements
+    zeroed there, and not given to anyone else before that stream is done with it."""
     if stream is not None:
         with torch.cuda.stream(stream):
-            return _new(shape, dtype, dev, None, zeroed)
-    t = torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
+            return _new(like, shape, dtype, None, zeroed)
+    t = like.new_empty(shape, dtype=dtype)
     if zeroed:
         t[:zeroed].zero_()
     return t
@@ -160,9 +160,9 @@ def qk_norm_rope(q, k=None, wq=None, wk=None, bq=None, bk=None, norm: int = NORM
         _is(t, name, torch.bfloat16, out_shape, optional=True)
     dev = _where(stream, "q k wq wk bq bk cos sin q_out k_out", q, k, wq, wk, bq, bk, cos, sin, q_out, k_out)
     if q is not None and q_out is None:
-        q_out = _new(out_shape, torch.bfloat16, dev, stream)
+        q_out = _new(q, out_shape, torch.bfloat16, stream)
     if k is not None and k_out is None:
-        k_out = _new(out_shape, torch.bfloat16, dev, stream)
+        k_out = _new(k, out_shape, torch.bfloat16, stream)
     _launch("sage_qk_norm_rope", dev, _p(q), _p(k), q_row, k_row, _p(wq), _p(bq), _p(wk), _p(bk),
             sage.DTYPE_F32 if w_dtype == torch.float32 else sage.DTYPE_BF16, _p(cos), _p(sin), B, N, H, d, int(norm),
             int(scope), float(eps), int(rope), int(rope_begin), rope_len, _p(q_out), _p(k_out), int(ranks),
@@ -197,11 +197,11 @@ def select_blocks(q, k, keep: int, first: int = 0, window: int = 0, lists=None, 
     _need(scratch, "scratch", torch.uint8, optional=True)
     dev = _where(stream, "q k lists counts scratch", q, k, lists, counts, scratch)
     if scratch is None:
-        scratch = _new(max(select_scratch_bytes(B, H, N, d), 16), torch.uint8, dev, stream)
+        scratch = _new(q, max(select_scratch_bytes(B, H, N, d), 16), torch.uint8, stream)
     if lists is None:
-        lists = _new((B, H, nT, keep), torch.int32, dev, stream)
+        lists = _new(q, (B, H, nT, keep), torch.int32, stream)
     if counts is None:
-        counts = _new((B, H, nT), torch.int32, dev, stream)
+        counts = _new(q, (B, H, nT), torch.int32, stream)
     _launch("sage_select_blocks", dev, _p(q), _p(k), B, H, N, d, int(keep), int(first), int(window), _p(lists),
             _p(counts), _p(scratch), scratch.numel(), _handle(stream, dev))
     return lists, counts
@@ -235,12 +235,12 @@ def attn_fwd_sparse(q, k, v, mode: int, lists, counts, coeff: int = COEFF_DIVIDE
     B, H, N, d = _sparse_args(q, k, v, o, lists, counts, workspace)
     dev = _where(stream, "q k v o lists counts workspace", q, k, v, o, lists, counts, workspace)
     if o is None:
-        o = _new((B, H, N, d), torch.bfloat16, dev, stream)
+        o = _new(q, (B, H, N, d), torch.bfloat16, stream)
     if workspace is None:
         n = sage.workspace_bytes(B, H, N, d, mode)
         if n == 0:
             raise SageError(EINVAL, "sage_workspace_bytes")
-        workspace = _new(n, torch.uint8, dev, stream, zeroed=256)       # the status words
+        workspace = _new(q, n, torch.uint8, stream, zeroed=256)       # the status words
     _launch("sage_attn_fwd_sparse", dev, _p(q), _p(k), _p(v), _p(o), B, H, N, d, int(mode), _p(lists),
             _p(counts), lists.shape[3], int(coeff), _p(workspace), workspace.numel() * workspace.element_size(), _handle(stream, dev))
     return o
@@ -249,7 +249,7 @@ def attn_fwd_sparse(q, k, v, mode: int, lists, counts, coeff: int = COEFF_DIVIDE
 def dbg_sparse_forced_timeout(q, k, v, mode: int, lists, counts, workspace, timeout_cycles: int, stream=None):
     B, H, N, d = _sparse_args(q, k, v, None, lists, counts, workspace)
     dev = _where(stream, "q k v lists counts workspace", q, k, v, lists, counts, workspace)
-    o = _new((B, H, N, d), torch.bfloat16, dev, stream)
+    o = _new(q, (B, H, N, d), torch.bfloat16, stream)
     _launch("sage_dbg_sparse_forced_timeout", dev, _p(q), _p(k), _p(v), _p(o), B, H, N, d, int(mode),
             _p(lists), _p(counts), lists.shape[3], COEFF_DIVIDE, _p(workspace), workspace.numel() * workspace.element_size(),
             int(timeout_cycles), _handle(stream, dev))
