@@ -20,7 +20,7 @@
 // Instructions come next: at 24 an element (norm, weights and rotation as
 // run-time choices inside the element loop, 64-bit token arithmetic) the kernel
 // was issue bound, 4.3 TB/s at 1 x 75600 x 40 x 128; hence the scope and the
-// pairing as template arguments, one form (x * r + t) * w for both norms in packed
+// pairing as template arguments, one form (x - mu) * r * w for both norms in packed
 // pairs, and one block per token with no division.
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -49,7 +49,8 @@ struct NrParams {
   const float4* sin4;
   int B, N, H, norm, w_f32, begin, len, ranks;   // len 0: no rotation
   uint32_t rank_mul;     // ceil(2^16 / heads of a rank): h * rank_mul >> 16 = h / heads of a rank for h < 256
-  float eps;
+  double inv_width;      // 1 / (H * d)
+  float inv_width_f32, eps;
 };
 
 __device__ __forceinline__ void nr_unpack(const uint4& u, float2 (&x)[4]) {
@@ -148,31 +149,33 @@ __global__ void __launch_bounds__(kNrThreads, CH == 5 ? (ALL ? 6 : 5) : 0) qk_no
     if (t.b) nr_weights(t.b, p.w_f32, l, bv);
   }
 
-  // y = x * r + shift before the weights
-  float r = 1.f, shift = 0.f;
+  // x becomes x - mu, and y = (x - mu) * r before the weights: a vector without variance is
+  // exactly 0, which x * r - mu * r, with mu * r rounded, is not.
+  float r = 1.f;
   if (ALL && p.norm != SAGE_NORM_NONE) {
-    const float inv = 1.f / (float)(p.H * D);
-    float mu = 0.f;
+    float2 s = make_float2(0.f, 0.f);
     if (p.norm == SAGE_NORM_LAYER) {
-      float2 s = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < CH; ++i)
 #pragma unroll
         for (int u = 0; u < 4; ++u) s = fadd2(s, x[i][u]);
-      mu = token_sum<TPT>(s.x + s.y, red) * inv;
+      // In fp64: for equal channels every partial sum is exact (at most 2^14 times a value of 8
+      // bits) and the mean must be that value; times fp32's 1 / width it may be its neighbour.
+      // (An fp32 division does as well, but spills at six blocks per SM.)
+      const float mu = __double2float_rn((double)token_sum<TPT>(s.x + s.y, red) * p.inv_width);
+      const float2 m2 = make_float2(mu, mu);
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[i][u] = fsub2(x[i][u], m2);
+      s = make_float2(0.f, 0.f);
     }
-    float2 s = make_float2(0.f, 0.f);
-    const float2 m2 = make_float2(mu, mu);
 #pragma unroll
     for (int i = 0; i < CH; ++i)
       if (i * TPT + lane < nvec)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float2 d = fsub2(x[i][u], m2);
-          s = ffma2v(d, d, s);
-        }
-    r = inv_root(token_sum<TPT>(s.x + s.y, red) * inv + p.eps);
-    shift = -mu * r;
+        for (int u = 0; u < 4; ++u) s = ffma2v(x[i][u], x[i][u], s);
+    r = inv_root(token_sum<TPT>(s.x + s.y, red) * p.inv_width_f32 + p.eps);
   }
 
   // the first chunk's output vector; in the plain layout a chunk is TPT / L heads further
@@ -193,11 +196,10 @@ __global__ void __launch_bounds__(kNrThreads, CH == 5 ? (ALL ? 6 : 5) : 0) qk_no
       float2 s = make_float2(0.f, 0.f);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const float2 d = fsub2(x[i][u], m2);
-        s = ffma2v(d, d, s);
+        x[i][u] = fsub2(x[i][u], m2);
+        s = ffma2v(x[i][u], x[i][u], s);
       }
       r = inv_root(head_sum<L>(s.x + s.y) * (1.f / (float)D) + p.eps);
-      shift = -mu * r;
     }
     if (p.norm != SAGE_NORM_NONE) {
       if (ALL && c < nvec) {
@@ -205,7 +207,7 @@ __global__ void __launch_bounds__(kNrThreads, CH == 5 ? (ALL ? 6 : 5) : 0) qk_no
         if (t.b) nr_weights(t.b, p.w_f32, c, bv);
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) x[i][u] = ffma2(x[i][u].x, x[i][u].y, r, shift);
+      for (int u = 0; u < 4; ++u) x[i][u] = fmul2(x[i][u], r);
       if (t.w)
 #pragma unroll
         for (int u = 0; u < 4; ++u) x[i][u] = fmul2v(x[i][u], wv[u]);
@@ -301,6 +303,8 @@ cudaError_t launch_qk_norm_rope(const void* q, const void* k, long long q_stride
   p.ranks = ranks;
   const int Hl = ranks > 0 ? H / ranks : H;
   p.rank_mul = (65536u + Hl - 1) / Hl;
+  p.inv_width = 1.0 / (H * d);
+  p.inv_width_f32 = 1.f / (float)(H * d);
   p.eps = eps;
   const bool half = rope == SAGE_ROPE_HALF;
   const int first = q ? 0 : 1, tensors = (q ? 1 : 0) + (k ? 1 : 0);
