@@ -1,0 +1,46 @@
+"""Bounded waits in the kernels' sources: what a wait that runs out must not leave behind (no GPU needed)."""
+import os
+import re
+
+import pytest
+
+from video_dit_quantized_b200 import build
+
+KERNELS = {"sparse.cu": 1, "attention.cu": 2, "linear.cu": 2, "select.cu": 1}     # kernels with bounded waits a file
+
+
+def source(name):
+    return re.sub(r"//[^\n]*", "", open(os.path.join(build.CSRC, name)).read())
+
+
+def kernels(name):
+    """The bodies of a file's kernels (up to the brace in the first column) that allocate tensor memory."""
+    out = [m.group(0) for m in re.finditer(r"__global__ void.*?\n}", source(name), flags=re.S)]
+    return [k for k in out if "tmem_alloc(" in k and not re.search(r"\bdbg_\w+_kernel\(", k)]
+
+
+def warp_parts(body):
+    """Where whole warps work: what follows the branch that one thread of a warp takes (softmax, epilogue)."""
+    start = max(body.rfind("regs_claim<"), body.rfind("else if (warp >= 4)"))
+    return body[start:] if start >= 0 else body
+
+
+@pytest.mark.parametrize("name", KERNELS)
+def test_a_warp_gives_a_wait_up_as_a_whole(name):
+    """A lane whose wait ran out must not leave while others go on into tcgen05.ld, a vote or a shuffle: there a wait
+    answers for the whole warp, or only sets the lane's step count to 0, which the loop and the epilogue vote on."""
+    found = kernels(name)
+    assert len(found) == KERNELS[name]
+    for body in found:
+        part = warp_parts(body)
+        assert re.search(r"tmem_ld\d+\(", part)
+        counted = False
+        for m in re.finditer(r"[^\n]*\bmbar_wait\([^\n]*", part):
+            line = m.group(0)
+            one_thread = "threadIdx.x == 0" in part[max(0, m.start() - 120):m.end()] or "&no_abort" in line
+            counts = re.search(r"if \([^\n]*!mbar_wait\([^\n]*\)\) steps = 0;$", line) is not None
+            assert "__all_sync" in line or one_thread or counts, line
+            counted |= counts
+        if counted:
+            assert "; __all_sync(0xffffffffu, j < steps); ++j)" in part
+            assert re.search(r"__all_sync\(0xffffffffu, steps == (nT|c)\)", part)

@@ -195,9 +195,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int qt = qt0 + t;
     const float sc = softmax_c(D);
     float m = -INFINITY, l = 0.f;
-    bool ok = true;
-    for (int j = 0; j < nT; ++j) {
-      if (!mbar_wait(&s_full[t], j & 1, abort_flag, limit)) { ok = false; break; }
+    // A lane whose wait ran out goes on, on scores that mean nothing, to the end of its step: the warp
+    // leaves as a whole, for tcgen05.ld, tcgen05.st and the votes need all its lanes.
+    int steps = nT;
+    for (int j = 0; __all_sync(0xffffffffu, j < steps); ++j) {
+      if (!mbar_wait(&s_full[t], j & 1, abort_flag, limit)) steps = 0;
       tc_fence_after();
       const int valid = min(128, N - j * 128);
       // the whole S row in registers (one wait for four loads)
@@ -235,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // part), so each one's compare phase overlaps the other's exponentials:
       // warpgroup 0 goes first, then they alternate.
       if (t == 1 || j > 0) {
-        if (!mbar_wait(&tok[t], (t == 0 ? (j - 1) : j) & 1, abort_flag, limit)) { ok = false; break; }
+        if (!mbar_wait(&tok[t], (t == 0 ? (j - 1) : j) & 1, abort_flag, limit)) steps = 0;
       }
       // p = 2^x, row sum (two packed accumulators), P packed as bf16 for the PV MMA
       float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
@@ -295,7 +297,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&p_full[t]);
     }
     // ---------------------------------------------------------- epilogue
-    if (ok && mbar_wait(&o_ready[t], 0, abort_flag, limit)) {
+    if (!mbar_wait(&o_ready[t], 0, abort_flag, limit)) steps = 0;
+    if (__all_sync(0xffffffffu, steps == nT)) {
       tc_fence_after();
       const int gq = qt * 128 + row;
       __nv_bfloat16* orow = prm.o + prm.o_map.row(bh, gq, N) * D;
@@ -517,13 +520,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     (void)ks_ext;
     float ks_next = SAGE_DCHECK((size_t)bh * nT, ks_ext, kSiteAttnKScale) ? prm.k_scale[(size_t)bh * nT] : 0.f;
     float m = -INFINITY, l = 0.f;
-    bool ok = true;
+    // A lane whose wait ran out goes on, on scores that mean nothing, to the end of its step: the warp
+    // leaves as a whole, for tcgen05.ld, tcgen05.st and the votes need all its lanes.
+    int steps = nT;
     uint32_t sr[128];
-    for (int j = 0; j < nT && ok; ++j) {
+    for (int j = 0; __all_sync(0xffffffffu, j < steps); ++j) {
       const float sc = __fmul_rn(__fmul_rn(qs, ks_next), c);
       if (j + 1 < nT && SAGE_DCHECK((size_t)bh * nT + j + 1, ks_ext, kSiteAttnKScale))
         ks_next = prm.k_scale[(size_t)bh * nT + j + 1];   // prefetch the next tile's scale
-      if (!mbar_wait(&s_full[t], j & 1, abort_flag, limit)) { ok = false; break; }
+      if (!mbar_wait(&s_full[t], j & 1, abort_flag, limit)) steps = 0;
       tc_fence_after();
 #pragma unroll
       for (int ch = 0; ch < 4; ++ch) tmem_ld32(tS + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[ch * 32]));
@@ -567,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the two warpgroups take turns on the exponential phase: warpgroup 0
       // first, then they alternate
       if (t == 1 || j > 0) {
-        if (!mbar_wait(&tok[t], (t == 0 ? (j - 1) : j) & 1, abort_flag, limit)) { ok = false; break; }
+        if (!mbar_wait(&tok[t], (t == 0 ? (j - 1) : j) & 1, abort_flag, limit)) steps = 0;
       }
       float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
       uint32_t pk[32];
@@ -604,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&tok[1 - t]);     // hand the exponential phase to the other warpgroup
       const bool grew = j > 0 && __any_sync(0xffffffffu, m_new > m);
       if (j > 0) {
-        if (!mbar_wait(&o_ready[t], (j - 1) & 1, abort_flag, limit)) { ok = false; break; }
+        if (!mbar_wait(&o_ready[t], (j - 1) & 1, abort_flag, limit)) steps = 0;
         tc_fence_after();
       }
 #pragma unroll
@@ -635,7 +640,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&p_full[t]);
     }
     // ---------------------------------------------------------- epilogue
-    if (ok && mbar_wait(&o_ready[t], (uint32_t)((nT - 1) & 1), abort_flag, limit)) {
+    if (!mbar_wait(&o_ready[t], (uint32_t)((nT - 1) & 1), abort_flag, limit)) steps = 0;
+    if (__all_sync(0xffffffffu, steps == nT)) {
       tc_fence_after();
       const int gq = qt * 128 + row;
       __nv_bfloat16* orow = prm.o + prm.o_map.row(bh, gq, N) * D;

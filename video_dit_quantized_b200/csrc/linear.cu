@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (kb + 32 < nk) load_window(kb + 32, xn, wn);
         }
         const float sc = __shfl_sync(0xFFFFFFFFu, sc_win, kb & 31);
-        if (!mbar_wait(&tfull[b], (uint32_t)(g >> 1) & 1u, abort_flag, limit)) {
+        if (!mbar_wait_warp(&tfull[b], (uint32_t)(g >> 1) & 1u, abort_flag, limit)) {
           ok = false;
           break;
         }
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n0 = nt * bf16g::BN + wg * 128;
       const int gm = mt * bf16g::BM + row;
       const bool live = n0 < prm.N && gm < prm.M;
-      if (!mbar_wait(&tfull[b], (uint32_t)(i >> 1) & 1u, abort_flag, limit)) break;
+      if (!mbar_wait_warp(&tfull[b], (uint32_t)(i >> 1) & 1u, abort_flag, limit)) break;
       tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {

@@ -72,6 +72,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// The same for a whole warp: all lanes go on or none does.  Where a wait runs out, one lane may see
+// its barrier complete while another gives up; single lanes must not leave in front of what a warp
+// does together (tcgen05.ld and st, votes, shuffles).  The votes are the loop's own conditions, so
+// the warp stays together.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                               long long limit) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const long long t0 = clock64();
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+    if (__any_sync(0xffffffffu, *abort_flag || clock64() - t0 > limit)) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
 // ---------------------------------------------------------------- TMA -------
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
   asm volatile(
