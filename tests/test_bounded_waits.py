@@ -44,3 +44,12 @@ def test_a_warp_gives_a_wait_up_as_a_whole(name):
         if counted:
             assert "; __all_sync(0xffffffffu, j < steps); ++j)" in part
             assert re.search(r"__all_sync\(0xffffffffu, steps == (nT|c)\)", part)
+
+
+@pytest.mark.parametrize("name", KERNELS)
+def test_what_is_in_flight_ends_before_the_block_does(name):
+    """The waits for a block's own loads and products at its end keep the long limit: the test hooks take limits of a
+    thousand clocks, which a load may exceed, and memory that a load still writes must not be given away."""
+    for body in kernels(name):
+        drains = re.findall(r"mbar_wait\([^\n]*&no_abort, (\w+)\)", body)
+        assert len(drains) >= 2 and set(drains) == {"kDefaultTimeoutCycles"}, drains

@@ -140,9 +140,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // drain: every load this thread issued must land before the CTA exits
       volatile int no_abort = 0;
-      mbar_wait(q_full, 0, &no_abort, limit);
+      mbar_wait(q_full, 0, &no_abort, kDefaultTimeoutCycles);
       for (int j = issued - C::STAGES < 0 ? 0 : issued - C::STAGES; j < issued; ++j)
-        mbar_wait(&kv_full[j % C::STAGES], (j / C::STAGES) & 1, &no_abort, limit);
+        mbar_wait(&kv_full[j % C::STAGES], (j / C::STAGES) & 1, &no_abort, kDefaultTimeoutCycles);
     } else if (warp == 1 && lane == 0) {
       // ---------------------------------------------------------- MMA issuer
       const uint32_t q_s = smem_u32(smem + C::OFF_Q);
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // drain: every MMA issued must complete before TMEM is released
       mma_commit(mma_done);
       volatile int no_abort = 0;
-      mbar_wait(mma_done, 0, &no_abort, limit);
+      mbar_wait(mma_done, 0, &no_abort, kDefaultTimeoutCycles);
     }
   } else {
     regs_claim<C::REGS_HIGH>();
@@ -424,9 +424,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // drain: every load this thread issued must land before the CTA exits
       volatile int no_abort = 0;
-      mbar_wait(q_full, 0, &no_abort, limit);
+      mbar_wait(q_full, 0, &no_abort, kDefaultTimeoutCycles);
       for (int j = issued - C::STAGES < 0 ? 0 : issued - C::STAGES; j < issued; ++j)
-        mbar_wait(&kv_full[j % C::STAGES], (j / C::STAGES) & 1, &no_abort, limit);
+        mbar_wait(&kv_full[j % C::STAGES], (j / C::STAGES) & 1, &no_abort, kDefaultTimeoutCycles);
     } else if (warp == 1 && lane == 0) {
       // ---------------------------------------------------------- MMA issuer
       const uint32_t q_s = smem_u32(smem + C::OFF_Q);
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // drain: every MMA issued must complete before TMEM is released
       mma_commit(mma_done);
       volatile int no_abort = 0;
-      mbar_wait(mma_done, 0, &no_abort, limit);
+      mbar_wait(mma_done, 0, &no_abort, kDefaultTimeoutCycles);
     }
   } else {
     regs_claim<C::REGS_HIGH>();

@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // drain: every load issued must land before the CTA exits
       volatile int no_abort = 0;
       for (long long j = g - STAGES < 0 ? 0 : g - STAGES; j < g; ++j)
-        mbar_wait(&full[j % STAGES], (uint32_t)(j / STAGES) & 1u, &no_abort, limit);
+        mbar_wait(&full[j % STAGES], (uint32_t)(j / STAGES) & 1u, &no_abort, kDefaultTimeoutCycles);
     } else if (warp == 1 && lane == 0) {
       // ---------------------------------------------------------- MMA issuer
       bool ok = true;
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // drain: every MMA issued must complete before TMEM is released
       mma_commit(mma_done);
       volatile int no_abort = 0;
-      mbar_wait(mma_done, 0, &no_abort, limit);
+      mbar_wait(mma_done, 0, &no_abort, kDefaultTimeoutCycles);
     }
   } else {
     regs_claim<REGS_HIGH>();
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     volatile int no_abort = 0;
     for (long long j = g - bf16g::STAGES < 0 ? 0 : g - bf16g::STAGES; j < g; ++j)
-      mbar_wait(&full[j % bf16g::STAGES], (uint32_t)(j / bf16g::STAGES) & 1u, &no_abort, limit);
+      mbar_wait(&full[j % bf16g::STAGES], (uint32_t)(j / bf16g::STAGES) & 1u, &no_abort, kDefaultTimeoutCycles);
   } else if (warp == 1 && lane == 0) {
     // ------------------------------------------------------------ MMA issuer
     bool ok = true;
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mma_commit(mma_done);
     volatile int no_abort = 0;
-    mbar_wait(mma_done, 0, &no_abort, limit);
+    mbar_wait(mma_done, 0, &no_abort, kDefaultTimeoutCycles);
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
     const int wg = (warp - 4) >> 2;

@@ -275,11 +275,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!go) break;
         id = next;
       }
-      // drain: every load this thread issued must land before the CTA exits
+      // drain: every load this thread issued must land before the CTA exits (given its own, long limit:
+      // a caller's may be shorter than a load takes)
       volatile int no_abort = 0;
-      if (nq > 0) mbar_wait(&b.q_full, (nq - 1) & 1, &no_abort, limit);
-      for (int i = max(0, nk - KS); i < nk; ++i) mbar_wait(&b.k_full[i % KS], (i / KS) & 1, &no_abort, limit);
-      for (int i = max(0, nv - VS); i < nv; ++i) mbar_wait(&b.v_full[i % VS], (i / VS) & 1, &no_abort, limit);
+      if (nq > 0) mbar_wait(&b.q_full, (nq - 1) & 1, &no_abort, kDefaultTimeoutCycles);
+      for (int i = max(0, nk - KS); i < nk; ++i) mbar_wait(&b.k_full[i % KS], (i / KS) & 1, &no_abort, kDefaultTimeoutCycles);
+      for (int i = max(0, nv - VS); i < nv; ++i) mbar_wait(&b.v_full[i % VS], (i / VS) & 1, &no_abort, kDefaultTimeoutCycles);
     } else if ((warp & 1) == 1 && lane_id == 0) {
       // ---------------------------------------------------------- MMA issuer of lane t
       const uint32_t q_s = smem_u32(smem + SC::OFF_Q + t * TILE);
@@ -334,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // drain: every MMA issued must complete before TMEM is released
       mma_commit(&mma_done[t]);
       volatile int no_abort = 0;
-      mbar_wait(&mma_done[t], 0, &no_abort, limit);
+      mbar_wait(&mma_done[t], 0, &no_abort, kDefaultTimeoutCycles);
     }
   } else {
     regs_claim<C::REGS_HIGH>();
