@@ -194,3 +194,20 @@ def test_ulysses_send_qk_on_the_host():
             assert torch.equal(sent[0][1], want)
         with pytest.raises(RuntimeError, match="v"):
             ua.attend_local()
+
+
+def test_products_of_other_widths_have_columns_of_their_own():
+    """Block scores: tcgen05 products run in issue order only where accumulator and shape are the same, so the three
+    products (48, 32 and 16 query columns) must not share tensor-memory columns."""
+    import os
+    from video_dit_quantized_b200 import build
+    txt = open(os.path.join(build.CSRC, "select.cu")).read()
+    rows = int(re.search(r"constexpr int kRows = (\d+);", txt).group(1))
+    cols = int(re.search(r"constexpr uint32_t kAccCols = (\d+);", txt).group(1))
+    expr = re.search(r"constexpr int acc_col\(int sl, int qs\) \{ return (.*?); \}", txt).group(1).replace("/", "//")
+    at = lambda sl, qs: eval(expr, dict(sl=sl, qs=qs, kRows=rows))
+    spans = [range(at(sl, 0), at(sl, 0) + rows * (3 - sl)) for sl in range(3)]
+    used = [c for s in spans for c in s]
+    assert len(set(used)) == len(used) == 6 * rows and max(used) < cols
+    assert [at(sl, qs) for sl in range(3) for qs in range(3 - sl)] == [s[qs * rows] for sl, s in enumerate(spans) for qs in range(3 - sl)]
+    assert "mma_ss<kKindI8>(tmem + acc_col(sl, 0)," in txt and "score_idesc(3 - sl), k > 0 ? 1u : 0u)" in txt

@@ -12,8 +12,7 @@
 // with a bound on their error decide nearly every row, and tensor cores give
 // them in exact integers: every mean is split into three 8-bit slices,
 //   x = step * (a0 + a1 / 2^7 + a2 / 2^14) + r,   step = amax / 127,   |r| <= 2^-14 step,
-// and the six products of weight up to 2^-14 are summed in int32 (tcgen05 kind::i8,
-// one accumulator a weight).  (All scores in fp64: 864 us at 1 x 40 x 75600 x 128; in
+// and the six products of weight up to 2^-14 are summed in int32 (tcgen05 kind::i8).  (All scores in fp64: 864 us at 1 x 40 x 75600 x 128; in
 // fp32 on the FMA pipe, bound by shared-memory wavefronts: 247 us; so: 98 us.)  Of the keys,
 // token 0's values are subtracted first, which shifts a row's scores alike and
 // makes amax, and with it the error, small where channels carry an offset.
@@ -205,6 +204,10 @@ constexpr int kScoreThreads = 256;
 constexpr int kRowRegs = 5;                // float4 of a row that a lane holds in registers
 constexpr int kKeys = 128;                 // key blocks of one tile: the MMA's M
 constexpr int kRows = 16;                  // query blocks of one tile: its N
+// Tensor-memory columns of the product of key slice sl and query slice qs: 48, 32 and 16 for the key slices.
+__host__ __device__ constexpr int acc_col(int sl, int qs) { return (sl * (7 - sl) / 2 + qs) * kRows; }
+constexpr uint32_t kAccCols = 128;
+static_assert(acc_col(1, 0) == 3 * kRows && acc_col(2, 0) == 5 * kRows && acc_col(2, 1) <= (int)kAccCols, "three products");
 __host__ __device__ constexpr uint32_t score_idesc(int slices) { return make_idesc(kFmtS32Acc, kFmtS8, kFmtS8, 0, kKeys, slices * kRows); }
 // Shared memory: 3 slices of a key tile (in the second pass: a row of 64-bit scores),
 // 3 slices of the query tile, the fp32 scores of ROWS <= 16 rows.
@@ -581,7 +584,7 @@ __global__ void __launch_bounds__(kScoreThreads, ROWS == kRows ? 2 : 1)
       tma_load_2d(sm + sl * C::KEY_BYTES, &tmK, &full, 0, ((3 + sl) * (int)gridDim.y + bh) * nT + x * kKeys);
   };
   if (warp == 1) {
-    tmem_alloc(&tmem_slot, 64);
+    tmem_alloc(&tmem_slot, kAccCols);
     tmem_relinquish();
   }
   if (threadIdx.x == 0) {
@@ -619,15 +622,15 @@ __global__ void __launch_bounds__(kScoreThreads, ROWS == kRows ? 2 : 1)
       ok = mbar_wait(&full, x & 1, &gave_up, kDefaultTimeoutCycles);
       tc_fence_after();
       const uint32_t a = smem_u32(sm), b = smem_u32(sm + C::OFF_Q);
-      // Key slice sl times query slices 0 .. 2 - sl, side by side as the columns of one product: accumulator
-      // w, of weight 2^-7w, collects those with sl + query slice = w.
+      // Key slice sl times query slices 0 .. 2 - sl, side by side as the columns of one product.  Each has
+      // columns of its own: products of other widths into the same columns have no order among them.
       if (ok)
 #pragma unroll
         for (int sl = 0; sl < 3; ++sl)
 #pragma unroll
           for (int k = 0; k < D / 32; ++k)
-            mma_ss<kKindI8>(tmem + sl * kRows, make_sdesc(a + sl * C::KEY_BYTES + k * 32, 16, 8 * D, C::LAYOUT),
-                            make_sdesc(b + k * 32, 16, 8 * D, C::LAYOUT), score_idesc(3 - sl), sl > 0 || k > 0 ? 1u : 0u);
+            mma_ss<kKindI8>(tmem + acc_col(sl, 0), make_sdesc(a + sl * C::KEY_BYTES + k * 32, 16, 8 * D, C::LAYOUT),
+                            make_sdesc(b + k * 32, 16, 8 * D, C::LAYOUT), score_idesc(3 - sl), k > 0 ? 1u : 0u);
       mma_commit(&done);
       ++committed;
     }
@@ -653,13 +656,22 @@ __global__ void __launch_bounds__(kScoreThreads, ROWS == kRows ? 2 : 1)
     }
     if (ok) {
       const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + r0;
-      uint32_t l0[8], l1[8], l2[8];
-      tmem_ld8(at, l0);
-      tmem_ld8(at + kRows, l1);
-      tmem_ld8(at + 2 * kRows, l2);
-      tmem_wait_ld_regs8(l0);
-      tmem_wait_ld_regs8(l1);
-      tmem_wait_ld_regs8(l2);
+      uint32_t c[3][3][8];                        // key slice, query slice
+#pragma unroll
+      for (int sl = 0; sl < 3; ++sl)
+#pragma unroll
+        for (int qs = 0; qs < 3 - sl; ++qs) tmem_ld8(at + acc_col(sl, qs), c[sl][qs]);
+#pragma unroll
+      for (int sl = 0; sl < 3; ++sl)
+#pragma unroll
+        for (int qs = 0; qs < 3 - sl; ++qs) tmem_wait_ld_regs8(c[sl][qs]);
+      // by weight 2^-7w: key slice + query slice = w
+      uint32_t (&l0)[8] = c[0][0], l1[8], l2[8];
+#pragma unroll
+      for (int r = 0; r < RH; ++r) {
+        l1[r] = c[0][1][r] + c[1][0][r];
+        l2[r] = c[0][2][r] + c[1][1][r] + c[2][0][r];
+      }
       float* to = scores + (size_t)r0 * p.nTp + j;
       if (j < p.nTp)
 #pragma unroll
@@ -686,7 +698,7 @@ __global__ void __launch_bounds__(kScoreThreads, ROWS == kRows ? 2 : 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem_slot, 64);
+  if (warp == 1) tmem_dealloc(tmem_slot, kAccCols);
   float kn = kmax_part[0][0], ks = kmax_part[1][0];
 #pragma unroll
   for (int w = 1; w < 4; ++w) {
