@@ -741,6 +741,10 @@ __global__ void __launch_bounds__(kScoreThreads, ROWS == kRows ? 2 : 1)
   }
 }
 
+constexpr size_t kSmemMax = 232448 - 2048;       // beside the static arrays
+// 4-row CTAs hold the longest rows
+static_assert(ScoreCfg<128>::smem(4, SAGE_SELECT_MAX_BLOCKS) <= kSmemMax, "the longest row must fit in shared memory");
+
 template <int D, int ROWS, int NV>
 cudaError_t score_launch(const SelectParams& p, int BH, cudaStream_t stream) {
   alignas(64) CUtensorMap tk, tq;
@@ -751,7 +755,9 @@ cudaError_t score_launch(const SelectParams& p, int BH, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   auto kern = score_select_kernel<D, ROWS, NV>;
   const int smem = (int)ScoreCfg<D>::smem(ROWS, p.nTp);
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // The limit is the function's, not the launch's: this call's own size, set by two host threads at
+  // once, could lower it between the other's setting and launch.
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
   if (e != cudaSuccess) return e;
   // its blocks may start, and set themselves up, while the pool kernel's last ones run
   cudaLaunchAttribute attr;
@@ -766,10 +772,6 @@ cudaError_t score_launch(const SelectParams& p, int BH, cudaStream_t stream) {
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, tk, tq, p);
 }
-
-constexpr size_t kSmemMax = 232448 - 2048;       // beside the static arrays
-// 4-row CTAs hold the longest rows
-static_assert(ScoreCfg<128>::smem(4, SAGE_SELECT_MAX_BLOCKS) <= kSmemMax, "the longest row must fit in shared memory");
 
 Pooled pooled_carve(void* base, int BH, int nT, int d) {
   const size_t rows = 2 * (size_t)BH * nT;
