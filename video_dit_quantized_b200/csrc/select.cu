@@ -281,7 +281,8 @@ struct ListOut {
     }
   }
   __device__ __forceinline__ void end(int lane) {
-    for (int s = done + lane; s < p.keep; s += 32)
+    // unsigned: a signed counter would wrap where keep is near 2^31
+    for (unsigned s = done + lane; s < (unsigned)p.keep; s += 32)
       if (SAGE_DCHECK(row + s, ext, kSiteSelectOut)) p.lists[row + s] = -1;
     if (lane == 0) p.counts[count] = done;
   }
