@@ -211,3 +211,22 @@ def test_products_of_other_widths_have_columns_of_their_own():
     assert len(set(used)) == len(used) == 6 * rows and max(used) < cols
     assert [at(sl, qs) for sl in range(3) for qs in range(3 - sl)] == [s[qs * rows] for sl, s in enumerate(spans) for qs in range(3 - sl)]
     assert "mma_ss<kKindI8>(tmem + acc_col(sl, 0)," in txt and "score_idesc(3 - sl), k > 0 ? 1u : 0u)" in txt
+
+
+def test_reads_ahead_in_a_list_end_with_it():
+    """Block-sparse attention reads a list two places ahead.  Widths go up to 2^31 - 1, so the place must be compared
+    without adding to the step in 32 bits (which wraps to a negative place, in front of the list)."""
+    import os
+    import numpy as np
+    from video_dit_quantized_b200 import build
+    txt = open(os.path.join(build.CSRC, "sparse.cu")).read()
+    assert len(re.findall(r"auto listed = \[&\]\(int j, int next\)", txt)) == 2
+    assert not re.search(r"listed\(j \+", txt)
+    bounds = re.findall(r"return (c|it\.steps) - j > next && SAGE_DCHECK", txt)
+    assert sorted(bounds) == ["c", "it.steps"]
+    for c in (1, 2, 3, 2 ** 31 - 1):
+        for j in {0, max(0, c - 3), max(0, c - 2), c - 1}:
+            for ahead in (0, 1, 2):
+                assert (np.int64(np.int32(c) - np.int32(j)) > ahead) == (j + ahead < c)
+    with np.errstate(over="ignore"):
+        assert np.int32(2 ** 31 - 2) + np.int32(2) < 0                        # what the sum would have been

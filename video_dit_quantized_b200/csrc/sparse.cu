@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         const long long off = (long long)id * prm.width;
-        auto listed = [&](int j) {
-          return j < c && SAGE_DCHECK(off + j, (long long)prm.items * prm.width, kSiteSparseList) ? __ldg(prm.lists + off + j) : 0;
+        auto listed = [&](int j, int next) {           // the block `next` places behind j (j + next may pass 2^31)
+          return c - j > next && SAGE_DCHECK(off + j + next, (long long)prm.items * prm.width, kSiteSparseList) ? __ldg(prm.lists + off + j + next) : 0;
         };
         // An index outside the sequence: the softmax masks its scores, and V must be zeros
         // (0 * inf would not be 0), which are read behind the end of the tensor.
@@ -255,13 +255,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++nv;
           return true;
         };
-        int cur = listed(0), ahead = listed(1);
+        int cur = listed(0, 0), ahead = listed(0, 1);
         if (!slot_free(nq, 1, &b.q_full, &b.q_empty)) break;
         load(&tmQ, q_dst, &b.q_full, it.bh, it.qb, false);
         ++nq;
         bool go = put_k(cur);
         for (int j = 0; j < c && go; ++j) {
-          const int after = listed(j + 2);             // read a step before its load
+          const int after = listed(j, 2);             // read a step before its load
           // the next item is asked for a few steps before this one's last load: early
           // enough to hide the counter's latency, late enough not to hoard work
           if (more && j == max(0, c - 3)) next = 2 * (int)gridDim.x + (int)atomicAdd(prm.next, 1u);
@@ -363,9 +363,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item it{0, 0, -1, 0};
     int blk_next = 0, blk_after = 0;                     // the next two blocks of its list
     float qs = 0.f, ks_next = 0.f, vsc = 0.f;            // QUANT: this row's Q scale, the next block's K scale, a V scale
-    auto listed = [&](int j) {
-      const long long at = ((long long)it.bh * nT + it.qb) * prm.width + j;
-      return j < it.steps && SAGE_DCHECK(at, (long long)prm.items * prm.width, kSiteSparseList) ? __ldg(prm.lists + at) : 0;
+    auto listed = [&](int j, int next) {                 // the block `next` places behind j (j + next may pass 2^31)
+      const long long at = ((long long)it.bh * nT + it.qb) * prm.width + j + next;
+      return it.steps - j > next && SAGE_DCHECK(at, (long long)prm.items * prm.width, kSiteSparseList) ? __ldg(prm.lists + at) : 0;
     };
     auto scale_of = [&](int x) {
       const long long ki = (long long)it.bh * nT + ((unsigned)x < (unsigned)nT ? x : 0);
@@ -376,8 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const volatile Item* vi = &b.item[n & 1];
       it = Item{vi->bh, vi->qb, vi->steps, vi->bad};
       mbar_arrive(&b.item_empty[n & 1]);
-      blk_next = listed(0);
-      blk_after = listed(1);
+      blk_next = listed(0, 0);
+      blk_after = listed(0, 1);
       if (QUANT && it.steps > 0) {
         const size_t qi = prm.q_per_token ? (size_t)it.bh * prm.Npad + it.qb * 128 + row : (size_t)it.bh * nT + it.qb;
         if (SAGE_DCHECK(qi, (long long)prm.BH * (prm.q_per_token ? prm.Npad : nT), kSiteSparseScale)) qs = __ldg(prm.q_scale + qi);
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int blk = blk_next;
         const float sc = QUANT ? __fmul_rn(__fmul_rn(qs, ks_next), softmax_c(D)) : softmax_c(D);
         blk_next = blk_after;
-        blk_after = listed(j + 2);
+        blk_after = listed(j, 2);
         ks_next = scale_of(blk_next);
         const int valid = (unsigned)blk < (unsigned)nT ? min(128, N - blk * 128) : 0;
         it.bad |= valid == 0;
