@@ -230,3 +230,21 @@ def test_reads_ahead_in_a_list_end_with_it():
                 assert (np.int64(np.int32(c) - np.int32(j)) > ahead) == (j + ahead < c)
     with np.errstate(over="ignore"):
         assert np.int32(2 ** 31 - 2) + np.int32(2) < 0                        # what the sum would have been
+
+
+@pytest.mark.parametrize("P", [1, 2])
+def test_ulysses_send_qk_refuses_what_it_sets_itself(P):
+    """On a stream of its own the norm would still be writing the send buffer when the exchange (or, with one rank,
+    attention) reads it: send_qk takes no stream, and no outputs or ranks, and starts nothing."""
+    from video_dit_quantized_b200.ulysses import UlyssesAttention
+    calls, sent = [], []
+    ua = UlyssesAttention(1, 8, 4, 16, P, mode=sage.MODE_BF16, device="cpu", permute=lambda *a: None,
+                          attention=lambda *a: None, a2a=lambda o, i: sent.append((o, i)),
+                          norm_rope=lambda q, k, **kw: calls.append(kw))
+    x = torch.zeros(1, 8, 4, 16, dtype=torch.bfloat16)
+    for name, value in (("stream", object()), ("stream", None), ("q_out", x), ("k_out", x), ("ranks", 2)):
+        with pytest.raises(ValueError, match=name):
+            ua.send_qk(x, x, **{name: value})
+    assert calls == [] and sent == [] and ua._pending == {} and ua._keep == {}
+    ua.send_qk(x, x, eps=1e-5)
+    assert len(calls) == 1 and calls[0]["eps"] == 1e-5 and len(sent) == (0 if P == 1 else 2)

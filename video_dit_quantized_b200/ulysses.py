@@ -99,9 +99,14 @@ class UlyssesAttention:
 
     def send_qk(self, q, k, **norm):
         """send() of q and k straight from the projections: their norm and position rotation (the arguments of
-        sparse.qk_norm_rope; the tables are those of this rank's tokens) write the send layout themselves, so no
-        copy runs before the all-to-alls."""
+        sparse.qk_norm_rope but for ranks, q_out, k_out and stream; the tables are those of this rank's tokens)
+        write the send layout themselves, so no copy runs before the all-to-alls.  Like send(), it works on the
+        current stream, which the all-to-alls and attention are ordered behind."""
         import torch
+        for name in ("ranks", "q_out", "k_out", "stream"):
+            if name in norm:
+                raise ValueError(f"send_qk sets {name} itself" if name != "stream" else
+                                 "send_qk works on the current stream: the exchange would not wait for another")
         shape = (self.B, self.Nl, self.H, self.d)
         for name, x in (("q", q), ("k", k)):
             if tuple(x.shape) != shape:
