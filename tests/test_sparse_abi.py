@@ -242,9 +242,9 @@ def test_ulysses_send_qk_refuses_what_it_sets_itself(P):
                           attention=lambda *a: None, a2a=lambda o, i: sent.append((o, i)),
                           norm_rope=lambda q, k, **kw: calls.append(kw))
     x = torch.zeros(1, 8, 4, 16, dtype=torch.bfloat16)
-    for name, value in (("stream", object()), ("stream", None), ("q_out", x), ("k_out", x), ("ranks", 2)):
+    for name, value in (("stream", object()), ("q_out", x), ("k_out", x), ("ranks", 2)):
         with pytest.raises(ValueError, match=name):
             ua.send_qk(x, x, **{name: value})
     assert calls == [] and sent == [] and ua._pending == {} and ua._keep == {}
-    ua.send_qk(x, x, eps=1e-5)
-    assert len(calls) == 1 and calls[0]["eps"] == 1e-5 and len(sent) == (0 if P == 1 else 2)
+    ua.send_qk(x, x, eps=1e-5, stream=None)
+    assert len(calls) == 1 and "stream" not in calls[0] and calls[0]["eps"] == 1e-5 and len(sent) == (0 if P == 1 else 2)

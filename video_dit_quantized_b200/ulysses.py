@@ -104,7 +104,7 @@ class UlyssesAttention:
         current stream, which the all-to-alls and attention are ordered behind."""
         import torch
         for name in ("ranks", "q_out", "k_out", "stream"):
-            if name in norm:
+            if norm.pop(name, None) is not None:
                 raise ValueError(f"send_qk sets {name} itself" if name != "stream" else
                                  "send_qk works on the current stream: the exchange would not wait for another")
         shape = (self.B, self.Nl, self.H, self.d)
