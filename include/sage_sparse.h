@@ -76,7 +76,9 @@ int sage_qk_norm_rope(const void* q, const void* k, long long q_stride, long lon
 /*
  * The key blocks of every 128-token query block, by a cheap score.  With
  * nT = ceil(N/128) and blocks of 128 tokens (the last one of the real rows only):
- *   qbar[i], kbar[j] = the mean of a block's rows, summed in fp64, rounded to fp32;
+ *   qbar[i], kbar[j] = the mean of a block's rows, summed in fp64 (rows r, r + 8, r + 16, ..
+ *                      for each r < 8, then the eight sums; exact, whatever the order, where a
+ *                      channel's nonzero values lie within a factor of 2^38), rounded to fp32;
  *   s[i][j] = sum over the d channels of qbar[i] * kbar[j], in fp64.
  * Row i keeps the min(keep, nT) blocks of largest s, ties to the lower index;
  * the blocks j < first and those with |i - j| <= window rank above all others

@@ -1,9 +1,11 @@
 // select.cu -- the key blocks each query block attends to, chosen by a cheap
 // score.
 //
-//   qbar_i, kbar_j = mean over the real rows of a 128-token block: exact sums
-//                    in fp64 (128 bf16 values span far less than 53 bits),
-//                    divided in fp64, rounded once to fp32;
+//   qbar_i, kbar_j = mean over the real rows of a 128-token block: summed in fp64
+//                    (rows r, r + 8, r + 16, .. for each r < 8, then the eight
+//                    sums), divided in fp64, rounded once to fp32.  Where a
+//                    channel's nonzero values lie within a factor of 2^38 of each
+//                    other the sum is exact, and the order does not matter;
 //   s_ij           = sum_c qbar_i[c] * kbar_j[c] in fp64;
 //   kept           = the `keep` largest s_ij of a row, ties to the lower j;
 //                    blocks j < first and |i - j| <= window rank above all.
