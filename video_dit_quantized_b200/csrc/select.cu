@@ -108,55 +108,51 @@ __global__ void __launch_bounds__(kPoolThreads<D>) pool_blocks_kernel(const uint
   const int c = threadIdx.x;
   const long long row = ((long long)blockIdx.z * gridDim.y + bh) * nT + blk, rows = 2LL * gridDim.y * nT;
   (void)rows;
-  float x = 0.f;                          // what is sliced
-  if (c < D) {
-    double t = 0.0;
+  double t = 0.0;
 #pragma unroll
-    for (int i = 0; i < GROUPS; ++i) t += part[i][c];
-    t /= (double)nr;
-    const float mean = __double2float_rn(t);
-    if (SAGE_DCHECK(row * D + c, rows * D, kSitePoolOut)) out.mean[row * D + c] = mean;
-    x = mean;
-    if (blockIdx.z == 1) {
-      const size_t at = (size_t)bh * N * D + c;      // token 0 of the head
-      if (SAGE_DCHECK(at / 8, ext, kSitePoolIn))
-        x = __double2float_rn(t - (double)__bfloat162float(reinterpret_cast<const __nv_bfloat16*>(k)[at]));
-    }
-    float sq = mean * mean, am = fabsf(x) < INFINITY ? fabsf(x) : INFINITY;
+  for (int i = 0; i < GROUPS; ++i) t += part[i][c];
+  t /= (double)nr;
+  const float mean = __double2float_rn(t);
+  if (SAGE_DCHECK(row * D + c, rows * D, kSitePoolOut)) out.mean[row * D + c] = mean;
+  float x = mean;                         // what is sliced
+  if (blockIdx.z == 1) {
+    const size_t at = (size_t)bh * N * D + c;      // token 0 of the head
+    if (SAGE_DCHECK(at / 8, ext, kSitePoolIn))
+      x = __double2float_rn(t - (double)__bfloat162float(reinterpret_cast<const __nv_bfloat16*>(k)[at]));
+  }
+  float sq = mean * mean, am = fabsf(x) < INFINITY ? fabsf(x) : INFINITY;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      sq += __shfl_xor_sync(0xffffffffu, sq, o);
-      am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-    }
-    if ((c & 31) == 0) {
-      norm_part[c >> 5] = sq;
-      amax_part[c >> 5] = am;
-    }
+  for (int o = 16; o > 0; o >>= 1) {
+    sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+  }
+  if ((c & 31) == 0) {
+    norm_part[c >> 5] = sq;
+    amax_part[c >> 5] = am;
   }
   __syncthreads();
-  if (c < D) {
-    float sq = norm_part[0], am = amax_part[0];
+  sq = norm_part[0];
+  am = amax_part[0];
 #pragma unroll
-    for (int i = 1; i < D / 32; ++i) {
-      sq += norm_part[i];
-      am = fmaxf(am, amax_part[i]);
-    }
-    // Not finite, or so small that squares and the reciprocal leave the normal range: an
-    // infinite step, and with it an infinite error bound, sends the rows to the second pass.
-    if (am > 0.f && am < 1e-15f) am = INFINITY;
-    const float y = am > 0.f && am < INFINITY ? fminf(fmaxf(x * (127.f / am), -127.f), 127.f) : 0.f;
-    const float a0 = rintf(y), r1 = (y - a0) * 128.f, a1 = rintf(r1), a2 = rintf((r1 - a1) * 128.f);
-    const long long slice = (long long)gridDim.y * nT * D;             // elements of one slice of one tensor
-    const long long at = blockIdx.z * 3 * slice + ((long long)bh * nT + blk) * D + c;
-    if (SAGE_DCHECK(at + 2 * slice, 6 * slice, kSitePoolOut)) {
-      out.slices[at] = (int8_t)a0;
-      out.slices[at + slice] = (int8_t)a1;
-      out.slices[at + 2 * slice] = (int8_t)a2;
-    }
-    if (c == 0 && SAGE_DCHECK(row, rows, kSitePoolOut)) {
-      out.step[row] = am / 127.f;
-      out.norm[row] = sqrtf(sq) * 1.001f;
-    }
+  for (int i = 1; i < D / 32; ++i) {
+    sq += norm_part[i];
+    am = fmaxf(am, amax_part[i]);
+  }
+  // Not finite, or so small that squares and the reciprocal leave the normal range: an
+  // infinite step, and with it an infinite error bound, sends the rows to the second pass.
+  if (am > 0.f && am < 1e-15f) am = INFINITY;
+  const float y = am > 0.f && am < INFINITY ? fminf(fmaxf(x * (127.f / am), -127.f), 127.f) : 0.f;
+  const float a0 = rintf(y), r1 = (y - a0) * 128.f, a1 = rintf(r1), a2 = rintf((r1 - a1) * 128.f);
+  const long long slice = (long long)gridDim.y * nT * D;             // elements of one slice of one tensor
+  const long long at = blockIdx.z * 3 * slice + ((long long)bh * nT + blk) * D + c;
+  if (SAGE_DCHECK(at + 2 * slice, 6 * slice, kSitePoolOut)) {
+    out.slices[at] = (int8_t)a0;
+    out.slices[at + slice] = (int8_t)a1;
+    out.slices[at + 2 * slice] = (int8_t)a2;
+  }
+  if (c == 0 && SAGE_DCHECK(row, rows, kSitePoolOut)) {
+    out.step[row] = am / 127.f;
+    out.norm[row] = sqrtf(sq) * 1.001f;
   }
 }
 
