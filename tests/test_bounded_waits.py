@@ -53,3 +53,18 @@ def test_what_is_in_flight_ends_before_the_block_does(name):
     for body in kernels(name):
         drains = re.findall(r"mbar_wait\([^\n]*&no_abort, (\w+)\)", body)
         assert len(drains) >= 2 and set(drains) == {"kDefaultTimeoutCycles"}, drains
+
+
+@pytest.mark.parametrize("name,columns", [("sparse.cu", "AHEAD"), ("attention.cu", "OVER")])
+def test_the_next_scores_wait_where_probabilities_lie_over_scores(name, columns):
+    """BF16 with D = 128 keeps P in S's columns.  tcgen05 orders products only where they share accumulator and shape,
+    so the product that reads P must be done before the next scores are written there; with D = 64, P lies beside S."""
+    body = [k for k in kernels(name) if "issue_pv_bf16" in k][0]
+    assert re.search(r"constexpr bool .*AHEAD = SC::AHEAD" if columns == "AHEAD" else r"constexpr bool OVER = D == 128;", body)
+    after_pv = body[body.index("issue_pv_bf16"):]
+    guard = re.search(r"if constexpr \((!AHEAD|OVER)\) \{(.*?)\n\s*\}", after_pv, flags=re.S)
+    commit, wait = guard.group(2).index("mma_commit(&"), guard.group(2).index("mbar_wait(&")
+    assert "p_read" in guard.group(2)[commit:commit + 25] and "p_read" in guard.group(2)[wait:wait + 25] and commit < wait
+    next_scores = re.search(r"issue_(s|qk<D, false>)\(", after_pv)
+    assert guard.start() + wait < next_scores.start()
+    assert re.search(r"(AHEAD \? tmem \+ 384 \+ t \* 64 : d_s|OVER \? tmem \+ t \* 128 : tmem \+ 384 \+ t \* 64)", body)

@@ -55,15 +55,17 @@ struct Params {
 };
 
 // BF16 mode: S = Q K^T and O += P V with kind::f16 (bf16 in, fp32 acc), P
-// rounded to bf16 and written over S in tensor memory.  P_t(j) overwrites
-// S_t(j), so QK_t(j+1) follows PV_t(j) in issue order; tcgen05 operations from
-// one thread execute in order and the commit after QK_t(j+1) also covers
-// PV_t(j), so S_t(j+1) implies O_t stable.
+// rounded to bf16 in tensor memory: beside S at D = 64, over S at D = 128, where
+// S and O fill it.  There QK_t(j+1) waits for PV_t(j), which reads P_t(j) where
+// the next S goes: products run in issue order only where they share the
+// accumulator and the shape.  (The wait costs 3 to 4%.)  The commit after
+// QK_t(j+1) also covers PV_t(j), so S_t(j+1) implies O_t stable.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const Params prm) {
   using C = Cfg<D, false>;
+  constexpr bool OVER = D == 128;                     // P lies over S
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -76,7 +78,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* tok = o_ready + 2;                        // [2] exp-phase token of softmax warpgroup t
   uint64_t* mma_done = tok + 2;
   uint64_t* never = mma_done + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
+  uint64_t* p_read = never + 1;                       // [2] OVER: PV_t has read P_t
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(p_read + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -96,6 +99,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&p_full[t], 128);
       mbar_init(&o_ready[t], 1);
       mbar_init(&tok[t], 128);
+      mbar_init(&p_read[t], 1);
     }
     mbar_init(mma_done, 1);
     mbar_init(never, 1);
@@ -162,12 +166,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int t = 0; t < 2; ++t) {
             if (!mbar_wait(&p_full[t], j & 1, abort_flag, limit)) { ok = false; break; }
             tc_fence_after();
-            issue_pv_bf16<D>(tmem + 256 + t * D, tmem + t * 128, v_s + s * C::TILE_BYTES, j > 0 ? 1u : 0u);
+            issue_pv_bf16<D>(tmem + 256 + t * D, OVER ? tmem + t * 128 : tmem + 384 + t * 64, v_s + s * C::TILE_BYTES, j > 0 ? 1u : 0u);
             if (j + 1 < nT) {
               const int s1 = (j + 1) % C::STAGES;
               if (t == 0 && !mbar_wait(&kv_full[s1], ((j + 1) / C::STAGES) & 1, abort_flag, limit)) {
                 ok = false;
                 break;
+              }
+              if constexpr (OVER) {
+                mma_commit(&p_read[t]);
+                if (!mbar_wait(&p_read[t], j & 1, abort_flag, limit)) { ok = false; break; }
               }
               issue_qk<D, false>(tmem + t * 128, q_s + t * C::TILE_BYTES, k_s + s1 * C::TILE_BYTES);
               mma_commit(&s_full[t]);
@@ -192,6 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t tS = tmem + lane_off + t * 128;
     const uint32_t tO = tmem + lane_off + 256 + t * D;
+    const uint32_t tP = OVER ? tS : tmem + lane_off + 384 + t * 64;
     const int qt = qt0 + t;
     const float sc = softmax_c(D);
     float m = -INFINITY, l = 0.f;
@@ -270,8 +279,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mbar_arrive(&tok[1 - t]);     // hand the exponential phase to the other warpgroup
       const bool grew = j > 0 && __any_sync(0xffffffffu, m_new > m);
-      tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-      tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+      tmem_st32(tP, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+      tmem_st32(tP + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
       // rescale O_t by alpha where the max grew (O_t is complete: the commit
       // after QK_t(j) covers PV_t(j-1))
       if (grew) {

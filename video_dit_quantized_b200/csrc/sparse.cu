@@ -109,6 +109,7 @@ struct Lane {
   uint64_t p_full;                  // P written, O rescaled
   uint64_t o_ready;                 // AHEAD: a PV done; else the item's last PV done
   uint64_t tok;                     // this lane's turn on the exponential phase
+  uint64_t p_read;                  // not AHEAD: a PV done, P's columns are free for the next S
   uint64_t item_full[2], item_empty[2];
 };
 
@@ -160,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&b.s_free, 128);
       mbar_init(&b.p_full, 128);
       mbar_init(&b.o_ready, 1);
+      mbar_init(&b.p_read, 1);
       mbar_init(&b.tok, 128);
       for (int s = 0; s < 2; ++s) {
         mbar_init(&b.item_full[s], 1);
@@ -310,8 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c == 0) continue;
         ok = mbar_wait(&b.q_full, nq & 1, abort_flag, limit);
         ++nq;
-        // the S columns are free: the previous item's last PV, which follows the
-        // softmax of its last S, is issued
+        // the S columns are free: the softmax of the previous item's last S comes before its last
+        // PV, which is issued (not AHEAD: done)
         ok = ok && issue_s(c == 1);
         for (int j = 0; j < c && ok; ++j) {
           // AHEAD: the next S as soon as this one is in the softmax warps' registers
@@ -327,9 +329,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             issue_pv_bf16<D>(d_o, d_p, v_s + (pv % VS) * TILE, j > 0 ? 1u : 0u);
           if (AHEAD || j + 1 == c) mma_commit(&b.o_ready);
           mma_commit(&b.v_empty[pv % VS]);
+          if constexpr (!AHEAD) {
+            // P lies over S, and a product into other columns has no order behind this one (tcgen05
+            // gives one only to products that share accumulator and shape): the next S, of the next
+            // item too, waits until P is read
+            mma_commit(&b.p_read);
+            ok = mbar_wait(&b.p_read, pv & 1, abort_flag, limit) && (j + 1 == c || issue_s(j + 2 == c));
+          }
           ++pv;
-          // else P lies over S, and operations of one thread execute in order
-          if (!AHEAD && j + 1 < c) ok = issue_s(j + 2 == c);
         }
       }
       // drain: every MMA issued must complete before TMEM is released
