@@ -99,13 +99,12 @@ __device__ __forceinline__ float head_sum(float v) {
 
 __device__ __forceinline__ float inv_root(float v) { return v == 0.f ? 0.f : rsqrtf(v); }
 
-// grid (ceil(N / TOKENS), tensors, B), TOKENS = kNrThreads / TPT.  The width of 5120
-// channels sits at 82 registers, one allocation step above six blocks per SM; held
-// below, 1 x 75600 x 40 x 128 over all heads takes 588 us (5.33 TB/s) instead of 622,
-// while per head (274 us at 32760 tokens) six blocks spill and five do not.  The other
-// widths are left to the compiler.
+// grid (ceil(N / TOKENS), tensors, B), TOKENS = kNrThreads / TPT.  Registers are left to the
+// compiler: 78 to 96 at 5120 channels, no spills.  Held to six blocks per SM (over all heads) or five
+// (per head), 1 x 75600 x 40 x 128 takes as long over all heads (548 us) and longer with half-split
+// pairs, which then spill (754 us, so: 659), and per head (594, so: 541).
 template <int D, int TPT, int CH, bool ALL, bool HALF>
-__global__ void __launch_bounds__(kNrThreads, CH == 5 ? (ALL ? 6 : 5) : 0) qk_norm_rope_kernel(const NrParams p, int first) {
+__global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(const NrParams p, int first) {
   constexpr int L = D / 8;                 // lanes of one head
   constexpr int TOKENS = kNrThreads / TPT;
   constexpr int F = HALF ? 2 : 1;          // float4 of factors a thread needs: 8 pairs (halves) or 4
@@ -161,7 +160,6 @@ __global__ void __launch_bounds__(kNrThreads, CH == 5 ? (ALL ? 6 : 5) : 0) qk_no
         for (int u = 0; u < 4; ++u) s = fadd2(s, x[i][u]);
       // In fp64: for equal channels every partial sum is exact (at most 2^14 times a value of 8
       // bits) and the mean must be that value; times fp32's 1 / width it may be its neighbour.
-      // (An fp32 division does as well, but spills at six blocks per SM.)
       const float mu = __double2float_rn((double)token_sum<TPT>(s.x + s.y, red) * p.inv_width);
       const float2 m2 = make_float2(mu, mu);
 #pragma unroll
