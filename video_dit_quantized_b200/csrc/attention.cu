@@ -10,7 +10,8 @@
 //                  P8 = e4m3(p*448) staged in shared memory, O += P8 V8
 //                  (kind::f8f6f4, fp32).
 //   attn_bf16_kernel: S = Q K^T and O += P V with kind::f16 (bf16 in, fp32
-//                  acc), P rounded to bf16 and kept in tensor memory over S.
+//                  acc), P rounded to bf16 and kept in tensor memory, beside S
+//                  (D = 64) or over it (D = 128).
 //
 // One CTA = two 128-row Q tiles of one (b, h) and every 128-key tile of that
 // head.  Warp roles (12 warps, registers re-split with setmaxnreg):
@@ -22,10 +23,11 @@
 //               rescaled in place in TMEM, and the epilogue.  The two
 //               warpgroups take turns on the exponential phase (an mbarrier
 //               token), so one's compare phase overlaps the other's ex2s.
-// TMEM (512 columns): S0 [0,128), S1 [128,256), O0 [256,256+D), O1 after it.
+// TMEM (512 columns): S0 [0,128), S1 [128,256), O0 [256,256+D), O1 after it; BF16 with
+// D = 64: P0 [384,448), P1 [448,512).
 //
 // Every wait is bounded (clock64 limit); a wait that runs out raises a
-// CTA-wide abort flag, every role leaves its loop, in-flight TMA loads and
+// CTA-wide abort flag, every role leaves its loop (a softmax warp as a whole), in-flight TMA loads and
 // MMAs are drained with bounded waits, TMEM is freed and the status word gets
 // kStatusTimeout.  No __trap, no unbounded spin.
 #include <cuda_bf16.h>

@@ -21,7 +21,7 @@
 // run-time choices inside the element loop, 64-bit token arithmetic) the kernel
 // was issue bound, 4.3 TB/s at 1 x 75600 x 40 x 128; hence the scope and the
 // pairing as template arguments, one form (x - mu) * r * w for both norms in packed
-// pairs, and one block per token with no division.
+// pairs, and one block per token with no division: 547 to 581 us (0.82 to 0.87 of a copy).
 #include <cuda_bf16.h>
 #include <cstdint>
 
@@ -259,7 +259,7 @@ cudaError_t nr_launch(const NrParams& p, bool all, bool half, int first, int ten
 
 // Threads per token by the width: up to 512 channels a warp (no block-wide sum), above
 // that a block of four (a warp with eight chunks a thread took 146 us where the block
-// with two takes 128: 2 x 17776 x 30 x 64, LAYER).
+// with two takes 128: 2 x 17776 x 30 x 64, LAYER per head).
 template <int D>
 cudaError_t nr_dispatch(const NrParams& p, bool all, bool half, int first, int tensors, cudaStream_t stream) {
   const int nvec = p.H * (D / 8);

@@ -14,10 +14,11 @@
 // with a bound on their error decide nearly every row, and tensor cores give
 // them in exact integers: every mean is split into three 8-bit slices,
 //   x = step * (a0 + a1 / 2^7 + a2 / 2^14) + r,   step = amax / 127,   |r| <= 2^-14 step,
-// and the six products of weight up to 2^-14 are summed in int32 (tcgen05 kind::i8).  (All scores in fp64: 864 us at 1 x 40 x 75600 x 128; in
-// fp32 on the FMA pipe, bound by shared-memory wavefronts: 247 us; so: 98 us.)  Of the keys,
-// token 0's values are subtracted first, which shifts a row's scores alike and
-// makes amax, and with it the error, small where channels carry an offset.
+// and the six products of weight up to 2^-14 are summed in int32 (tcgen05 kind::i8).  (All
+// scores in fp64: 864 us at 1 x 40 x 75600 x 128; in fp32 on the FMA pipe, bound by
+// shared-memory wavefronts: 247 us; so: 98 us.)  Of the keys, token 0's values are
+// subtracted first, which shifts a row's scores alike and makes amax, and with it the error,
+// small where channels carry an offset.
 //
 // Two kernels.  pool: one CTA per (block, head, tensor), HBM-bound, q and k are
 // read once; it writes the means, their slices, steps and norms.  score: one CTA
@@ -28,8 +29,8 @@
 // a third of it the products' reads of the key slices from shared memory (each slice is
 // read once for all query slices: the products took twice as long with one each), and
 // a row's selection 5,000, 13,000 where scores are refined.
-// The call at 1 x 40 x 75600 x 128: 360 us (4.3 TB/s), the pool kernel of it 262 (5.9 TB/s,
-// 0.90 of a copy); 1 x 30 x 17776 x 64: 44 us.
+// The call at 1 x 40 x 75600 x 128: 363 to 366 us (4.3 TB/s), the pool kernel of it 262
+// (5.9 TB/s, 0.90 of a copy); 1 x 30 x 17776 x 64: 47 us, 44 on the device.
 //   |computed - exact| <= E = 3 step_q max step_k + 2^-23 |qbar| max |kbar|:
 //   the products left out are below 0.51 step_q step_k (128 * 2 * 64 * 64 * 2^-21), the
 //   remainders r below 128 * 127 * 2 * 4.7e-5 = 1.53, four fp32 roundings of at most
@@ -39,7 +40,9 @@
 //   Else the rows' order is open only among scores in [a - 2 E, b + 2 E]: up to 32 of
 //   them are computed in fp64 by the warp and ranked (9% of the rows); more (equal or
 //   all-zero blocks, values that are not finite) send the row to a second pass, in
-//   which the CTA computes the whole row in fp64 and bisects over its bits.
+//   which the CTA computes the whole row in fp64 and bisects over its bits.  Its rows go one
+//   after another: with all blocks equal the call above takes 4.9 ms, with the last quarter
+//   of the tokens zero 3.3 ms.
 #include <cuda_bf16.h>
 #include <algorithm>
 #include <cmath>
@@ -808,7 +811,8 @@ cudaError_t select_d(const void* q, const void* k, int BH, int N, int keep, int 
   const SelectParams p{pooled, nT, nTp, keep, first, std::min(window, nT), (float)z, slope, lists, counts};
   // A warp's row in registers while a lane's stretch is at most 20 blocks (read again for
   // every threshold the call takes 401 us at 1 x 40 x 75600 x 128, in registers 375);
-  // sixteen rows a CTA, two CTAs per SM, while their scores fit; four for longer rows.
+  // sixteen rows a CTA, two CTAs per SM, while their scores fit; four for longer rows (1 x 4 x
+  // 332800 x 128, 2600 blocks, sixteen rows: 414 us; 1 x 4 x 384000 x 128, four: 634 us).
   if (nTp <= 128 * kRowRegs) return score_launch<D, kRows, kRowRegs>(p, BH, stream);
   if (ScoreCfg<D>::smem(kRows, nTp) <= kSmemMax) return score_launch<D, kRows, 0>(p, BH, stream);
   return score_launch<D, 4, 0>(p, BH, stream);

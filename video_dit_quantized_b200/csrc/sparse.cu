@@ -22,23 +22,27 @@
 //                item's epilogue.
 // One thread per lane and task, each in blocking waits: one thread polling for
 // both lanes added its poll to every step of the BF16 kernel, whose steps are a
-// chain S -> P -> PV -> S (6,000 clocks a step against 4,800).
+// chain S -> P -> PV -> S (a quarter longer).
 // Where P has a place of its own (QUANT: shared memory; BF16 with D = 64: the
 // tensor memory that the shorter O leaves) the next S is formed while this one is
-// in the softmax: 4,040 clocks for a step of both lanes become 3,630 (BF16, D = 64).
+// in the softmax: a step takes 10% less (BF16, D = 64).  Elsewhere the next S waits
+// until PV has read P in its columns (2.3 to 3%; formed in two halves, the one beside P
+// ahead of the wait, 9% more: products of half the width).
 // The two softmax warpgroups take turns on the exponential phase (an mbarrier
 // token, strictly alternating; a lane that has run out of items gives its turns
-// away), except in BF16 with D = 64.  Clocks for a step of both lanes with and
-// without turns: QUANT 3,770 and 4,220 (D = 64), 3,750 and 4,310 (D = 128); BF16
-// 5,010 and 5,540 (D = 128), but 3,630 and 3,230 (D = 64), where neither the MMAs nor
-// the packing of P hold the other lane up.  2,048 of them are the exponentials.
+// away), except in BF16 with D = 64.  Without turns a step of both lanes takes 12%
+// (QUANT, D = 64), 15% (QUANT, D = 128) and 11% (BF16, D = 128) longer, but 11% less in
+// BF16 with D = 64, where neither the MMAs nor the packing of P hold the other lane up.
 // K and V tiles have rings of their own: K_j is free once Q K_j^T is done, a
 // whole step before V_j.
-// What bounds it: the exponentials' schedule (55% of the SFU rate INT8/FP8, 65% BF16 with
-// D = 64), in BF16 with D = 128 the chain of a lane, and the power limit.  Measured, the
-// prepass included: 1 x 40 x 75600 x 128, 59 of 591 blocks a row, INT8/FP8 10.5 to 11.0 ms;
-// BF16 1 x 30 x 17776 x 64, 28 of 139 blocks, 750 us; 1 x 12 x 32760 x 128, lists of up to
-// 64 of 256 blocks, 1.01 ms.
+// What bounds it: the exponentials' schedule (56% of the SFU rate INT8/FP8, 64% BF16 with
+// D = 64), in BF16 with D = 128 the chain of a lane, and the power limit.  Clocks for a step
+// of both lanes, items' ends and tail included (time x SM clock x SMs / half the steps; the
+// dense kernels by the same reckoning in brackets): INT8/FP8 3,960 (3,470) at D = 128, 4,110
+// (3,750) at D = 64; BF16 4,640 (4,190) and 3,600 (3,710).  2,048 of them are the
+// exponentials.  Measured, the prepass included: 1 x 40 x 75600 x 128, 59 of 591 blocks a
+// row, INT8/FP8 10.5 to 11.0 ms; BF16 1 x 30 x 17776 x 64, 28 of 139 blocks, 720 to 770 us;
+// 1 x 12 x 32760 x 128, lists of up to 64 of 256 blocks, 1.02 to 1.04 ms.
 //
 // A listed index outside [0, ceil(N/128)) adds nothing to its row and a count
 // outside [0, width] is clamped to it; both are recorded in the status word and
